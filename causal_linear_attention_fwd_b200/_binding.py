@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import json
+import math
 import os
 import threading
 
@@ -20,11 +21,18 @@ LIB_PATH = os.path.join(HERE, "libla2.so")
 LA2_OK, LA2_ERR_INVALID, LA2_ERR_UNSUPPORTED, LA2_ERR_CUDA, LA2_ERR_TIMEOUT = range(5)
 LA2_F32, LA2_BF16 = 0, 1
 LA2_OP_FORWARD, LA2_OP_BACKWARD, LA2_OP_SHARD_STATE, LA2_OP_DLAMBDA = 0, 1, 2, 3
+LA2_OP_GATED_NORM_BACKWARD, LA2_OP_RESIDUAL_NORM_BACKWARD = 4, 5
 LA2_OPT_SPLIT, LA2_OPT_PATH, LA2_OPT_INJECT_TIMEOUT, LA2_OPT_VARIANT, LA2_OPT_TRACE = 0, 1, 2, 3, 4
 LA2_OPT_VARLEN_ORDER, LA2_OPT_DECODE_BLOCK_TOKENS, LA2_OPT_BWD_FORM = 5, 6, 7
 
 _lock = threading.Lock()
 _lib = None
+
+
+class _Heads(ctypes.Structure):
+    """la2_heads: a [B, heads, L, width] tensor by its first value and strides."""
+    _fields_ = [("p", ctypes.c_void_p), ("batch", ctypes.c_int64), ("head", ctypes.c_int64),
+                ("row", ctypes.c_int64)]
 
 
 class LA2Error(RuntimeError):
@@ -85,6 +93,24 @@ def library():
         lib.la2_feature_map.restype = I
         lib.la2_feature_map_backward.argtypes = [P, P, P, P, P, P, I64, I, P]
         lib.la2_feature_map_backward.restype = I
+        HP, F, U = ctypes.POINTER(_Heads), ctypes.c_float, ctypes.c_uint
+        lib.la2_rotary.argtypes = [HP, HP, HP, P, P, I, P, P, P, F, U, I, I, I, I64, I, I, I, I, P]
+        lib.la2_rotary.restype = I
+        lib.la2_rotary_backward.argtypes = [P, P, P, P, P, I, HP, HP, HP, F, U, I, I, I, I64, I, I,
+                                            I, I, P]
+        lib.la2_rotary_backward.restype = I
+        lib.la2_gated_norm.argtypes = [P, P, I64, I64, P, P, F, U, I, I, I64, I, I, P]
+        lib.la2_gated_norm.restype = I
+        lib.la2_gated_norm_backward.argtypes = [P, P, P, I64, I64, P, P, P, I64, I64, P, F, U, I, I,
+                                                I64, I, I, P, SZ, P]
+        lib.la2_gated_norm_backward.restype = I
+        lib.la2_residual_norm.argtypes = [P, I, P, P, P, P, P, F, F, F, U, I64, I, I, P]
+        lib.la2_residual_norm.restype = I
+        lib.la2_residual_norm_backward.argtypes = [P, P, P, I, P, P, P, P, P, P, P, F, F, F, U, I64,
+                                                   I, I, P, SZ, P]
+        lib.la2_residual_norm_backward.restype = I
+        lib.la2_pool_copy.argtypes = [P, I, P, I, P, P, I, I, I, I, I, P]
+        lib.la2_pool_copy.restype = I
         lib.la2_last_device_error.argtypes = [P]
         lib.la2_last_device_error.restype = I
         lib.la2_status_string.argtypes = [I]
@@ -576,6 +602,368 @@ def feature_map_backward(q, k, dphi_q, dphi_k=None, *, out=None, stream=None):
                                             _stream(stream, dev))
     _check(code, "la2_feature_map_backward")
     return dq if k is None else (dq, dk)
+
+
+LA2_ROTARY_INTERLEAVED = 1
+LA2_POSITIONS_ROW, LA2_POSITIONS_START, LA2_POSITIONS_TABLE = 0, 1, 2
+LA2_NORM_SILU, LA2_NORM_ROW, LA2_NORM_SHARED_WEIGHT, LA2_NORM_POST = 1, 2, 4, 8
+
+
+def _like(dev, **named):
+    """CUDA tensors (None skipped) on `dev`, any strides."""
+    for name, t in named.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+
+
+def _strides(name, t, dims):
+    """The strides of a tensor's leading `dims` axes; its last axis is dense.
+    An axis of one entry has no stride that matters."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    return [0 if t.shape[i] <= 1 else t.stride(i) for i in range(dims)]
+
+
+def _heads(name, t):
+    return _Heads(t.data_ptr(), *_strides(name, t, 3))
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, factor: float = 1.0,
+                       scaling: str = "none", original_length: int = 8192, fast: float = 32.0,
+                       slow: float = 1.0, device="cuda"):
+    """(inv_freq, scale) for rotary(): inv_freq float64 [rotary_dim / 2], pair
+    i's angle per position, base^(-2i / rotary_dim), and the number that q and
+    k are multiplied by.  For contexts `factor` times as long as the
+    `original_length` a model was trained on, scaling is
+      "none"      as trained;
+      "linear"    every position divided by factor;
+      "base"      the base raised so that the slowest pair turns 1 / factor as
+                  fast and the fastest keeps its pace;
+      "by_parts"  pairs that turn more than `fast` times over original_length
+                  kept, those that turn less than `slow` times slowed down by
+                  factor, a linear blend between, and scale = 1 + 0.1 ln
+                  factor."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and at least 2")
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base must be above 1 and factor at least 1")
+    if scaling not in ("none", "linear", "base", "by_parts"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    n = rotary_dim // 2
+    if scaling == "base" and n > 1:
+        base *= factor ** (rotary_dim / (rotary_dim - 2))
+    f = [base ** (-2.0 * i / rotary_dim) for i in range(n)]
+    scale = 1.0
+    if scaling == "linear":
+        f = [x / factor for x in f]
+    elif scaling == "by_parts":
+        if not fast > slow > 0.0 or original_length < 1:
+            raise ValueError("fast must be above slow, slow above 0 and original_length at least 1")
+        for i, x in enumerate(f):
+            turns = original_length * x / (2.0 * math.pi)
+            keep = min(1.0, max(0.0, (turns - slow) / (fast - slow)))
+            f[i] = x * (keep + (1.0 - keep) / factor)
+        scale = 1.0 + 0.1 * math.log(factor)
+    return torch.tensor(f, dtype=torch.float64, device=device), scale
+
+
+def _rotary_args(inv_freq, positions, B, L, dev):
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be float64 [rotary_dim / 2]")
+    kind = LA2_POSITIONS_ROW
+    if positions is not None:
+        if positions.dtype != torch.int64 or tuple(positions.shape) not in ((B,), (B, L)):
+            raise ValueError("positions must be int64 [B] or [B,L]")
+        kind = LA2_POSITIONS_START if positions.dim() == 1 else LA2_POSITIONS_TABLE
+    if _devices(("inv_freq", inv_freq), ("positions", positions)) != dev:
+        raise ValueError(f"inv_freq is on {inv_freq.device}, other arguments on {dev}")
+    return kind
+
+
+def rotary(q, k, inv_freq, positions=None, *, v=None, interleaved: bool = False,
+           scale: float = 1.0, out=None, stream=None):
+    """Rotary positions on q and k on their way from a projection to the
+    attention.  q [B,H,L,d], k [B,Hk,L,d] and v [B,Hk,L,e] may be strided views
+    (of a fused token-major projection, say) with contiguous columns; the
+    results are contiguous [B,H,L,.] as forward() and decode_tokens() take them,
+    k and v heads shared by H / Hk q heads repeated.  The first 2 *
+    len(inv_freq) columns of every head turn (halves paired, or neighbours when
+    interleaved) and are multiplied by scale; see rotary_frequencies().
+    positions: None (row t is position t), int64 [B] (row t of request b is
+    positions[b] + t) or int64 [B,L].  Returns (rq, rk), or with v (rq, rk, rv);
+    out: buffers for them."""
+    lib = library()
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    dev = q.device
+    _like(dev, k=k, v=v)
+    B, H, L, d = q.shape
+    Hk, e = k.shape[1], (d if v is None else v.shape[-1])
+    if tuple(k.shape) != (B, Hk, L, d) or (v is not None and tuple(v.shape) != (B, Hk, L, e)):
+        raise ValueError("q must be [B,H,L,d], k [B,Hk,L,d] and v [B,Hk,L,e]")
+    if H != Hk and (Hk == 0 or H % Hk):
+        raise ValueError("H must be a multiple of Hk")
+    if k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+        raise ValueError("q, k and v must have one dtype")
+    kind = _rotary_args(inv_freq, positions, B, L, dev)
+    with torch.cuda.device(dev):
+        shapes = ((B, H, L, d), (B, H, L, d), (B, H, L, e))[:2 if v is None else 3]
+        if out is None:
+            outs = [torch.empty(s, dtype=q.dtype, device=dev) for s in shapes]
+        else:
+            if len(out) != len(shapes):
+                raise ValueError(f"out must be {len(shapes)} buffers")
+            outs = [_out(t, f"out[{i}]", s, q.dtype, dev) for i, (t, s) in enumerate(zip(out, shapes))]
+        code = lib.la2_rotary(_ref(_heads("q", q)), _ref(_heads("k", k)),
+                              None if v is None else _ref(_heads("v", v)), _ptr(inv_freq),
+                              _ptr(positions), kind, _ptr(outs[0]), _ptr(outs[1]),
+                              None if v is None else _ptr(outs[2]), float(scale),
+                              LA2_ROTARY_INTERLEAVED if interleaved else 0, B, H, Hk, L, d, e,
+                              2 * inv_freq.numel(), _dt(q), _stream(stream, dev))
+    _check(code, "la2_rotary")
+    return tuple(outs)
+
+
+def rotary_backward(dq, dk, inv_freq, positions=None, *, dv=None, kv_heads=None,
+                    interleaved: bool = False, scale: float = 1.0, out=None, stream=None):
+    """Chain rule through rotary(): dq, dk [B,H,L,d] (and dv [B,H,L,e]) are
+    the attention's gradients; returns the gradients (gq [B,H,L,d], gk
+    [B,kv_heads,L,d][, gv [B,kv_heads,L,e]]) of its inputs, those of a shared
+    head summed over its q heads.  kv_heads: H when None.  out: tensors of
+    those shapes to write, strided views allowed (slices of a fused
+    projection's gradient); by default views of token-major [B,L,heads,.]
+    buffers."""
+    lib = library()
+    dev = _devices(("dq", dq), ("dk", dk), ("dv", dv))
+    B, H, L, d = dq.shape
+    Hk, e = H if kv_heads is None else int(kv_heads), (d if dv is None else dv.shape[-1])
+    if dk.shape != dq.shape or (dv is not None and tuple(dv.shape) != (B, H, L, e)):
+        raise ValueError("dq, dk must be [B,H,L,d] and dv [B,H,L,e]")
+    if Hk < 0 or (H != Hk and (Hk == 0 or H % Hk)):
+        raise ValueError("H must be a multiple of kv_heads")
+    if dk.dtype != dq.dtype or (dv is not None and dv.dtype != dq.dtype):
+        raise ValueError("dq, dk and dv must have one dtype")
+    kind = _rotary_args(inv_freq, positions, B, L, dev)
+    with torch.cuda.device(dev):
+        shapes = ((B, H, L, d), (B, Hk, L, d), (B, Hk, L, e))[:2 if dv is None else 3]
+        if out is None:
+            outs = [torch.empty((b, n, h, w), dtype=dq.dtype, device=dev).transpose(1, 2)
+                    for b, h, n, w in shapes]
+        else:
+            if len(out) != len(shapes):
+                raise ValueError(f"out must be {len(shapes)} tensors")
+            outs = list(out)
+            for i, (t, s) in enumerate(zip(outs, shapes)):
+                _like(dev, **{f"out[{i}]": t})
+                if tuple(t.shape) != s or t.dtype != dq.dtype:
+                    raise ValueError(f"out[{i}] must be {dq.dtype} {s}")
+        views = [_heads(f"out[{i}]", t) for i, t in enumerate(outs)]
+        code = lib.la2_rotary_backward(_ptr(dq), _ptr(dk), _ptr(dv), _ptr(inv_freq),
+                                       _ptr(positions), kind, _ref(views[0]), _ref(views[1]),
+                                       None if dv is None else _ref(views[2]), float(scale),
+                                       LA2_ROTARY_INTERLEAVED if interleaved else 0, B, H, Hk, L,
+                                       d, e, 2 * inv_freq.numel(), _dt(dq), _stream(stream, dev))
+    _check(code, "la2_rotary_backward")
+    return tuple(outs)
+
+
+def _gated_args(o, gate, weight, activation, per_head, dev):
+    B, H, L, e = o.shape
+    if activation not in ("silu", "sigmoid"):
+        raise ValueError(f"unknown activation {activation!r}")
+    flags = (LA2_NORM_SILU if activation == "silu" else 0) | (0 if per_head else LA2_NORM_ROW)
+    _like(dev, gate=gate)
+    if gate is not None and (tuple(gate.shape) != (B, L, H * e) or gate.dtype != o.dtype):
+        raise ValueError("gate must be [B,L,H*e] of o's dtype")
+    if weight is not None:
+        if weight.dtype != torch.float32 or weight.dim() != 1:
+            raise ValueError("weight must be float32 [H*e] or [e]")
+        if per_head and weight.numel() == e:
+            flags |= LA2_NORM_SHARED_WEIGHT
+        elif weight.numel() != H * e:
+            raise ValueError("weight must be float32 [H*e], or [e] for a norm per head")
+    return B, H, L, e, flags
+
+
+def gated_norm(o, gate=None, weight=None, *, activation: str = "silu", per_head: bool = True,
+               eps: float = 1e-6, out=None, stream=None):
+    """The attention's output normed and gated for the output projection:
+    u = o / sqrt(mean(o^2) + eps) * weight * a(gate), o [B,H,L,e] to u
+    [B,L,H*e], the mean over each head's columns or (per_head False) over the
+    token's whole row.  gate [B,L,H*e] may be a view with strided batches and
+    rows (a slice of a fused projection); a is "silu" or "sigmoid".  weight
+    float32 [H*e], or [e] for all heads alike (per head only), or None."""
+    lib = library()
+    dev = _devices(("o", o), ("weight", weight))
+    B, H, L, e, flags = _gated_args(o, gate, weight, activation, per_head, dev)
+    with torch.cuda.device(dev):
+        u = (_out(out, "out", (B, L, H * e), o.dtype, dev) if out is not None
+             else torch.empty((B, L, H * e), dtype=o.dtype, device=dev))
+        sb, sl = (0, 0) if gate is None else _strides("gate", gate, 2)
+        code = lib.la2_gated_norm(_ptr(o), _ptr(gate), sb, sl, _ptr(weight), _ptr(u), float(eps),
+                                  flags, B, H, L, e, _dt(o), _stream(stream, dev))
+    _check(code, "la2_gated_norm")
+    return u
+
+
+def gated_norm_backward(du, o, gate=None, weight=None, *, activation: str = "silu",
+                        per_head: bool = True, eps: float = 1e-6, out=None, workspace=None,
+                        stream=None):
+    """Gradients (do, dgate, dweight) of gated_norm's inputs from du
+    [B,L,H*e]; dgate is None without a gate, dweight (float32, of weight's
+    shape) None without a weight.  out: (do, dgate) to write; dgate may be a
+    view with strided batches and rows."""
+    lib = library()
+    dev = _devices(("du", du), ("o", o), ("weight", weight), ("workspace", workspace))
+    B, H, L, e, flags = _gated_args(o, gate, weight, activation, per_head, dev)
+    if tuple(du.shape) != (B, L, H * e) or du.dtype != o.dtype:
+        raise ValueError("du must be [B,L,H*e] of o's dtype")
+    with torch.cuda.device(dev):
+        if out is not None:
+            do, dgate = out
+            _out(do, "do", o.shape, o.dtype, dev)
+            if (dgate is None) != (gate is None):
+                raise ValueError("gate and dgate are both given or both None")
+            _like(dev, dgate=dgate)
+            if dgate is not None and (dgate.shape != gate.shape or dgate.dtype != o.dtype):
+                raise ValueError("dgate must match gate's shape and dtype")
+        else:
+            do = torch.empty_like(o)
+            dgate = None if gate is None else torch.empty((B, L, H * e), dtype=o.dtype, device=dev)
+        dw = None if weight is None else torch.empty_like(weight)
+        if workspace is None and dw is not None:
+            workspace = _workspace(
+                workspace_size(LA2_OP_GATED_NORM_BACKWARD, B, H, L, e, e, o.dtype), dev)
+        sb, sl = (0, 0) if gate is None else _strides("gate", gate, 2)
+        tb, tl = (0, 0) if gate is None else _strides("dgate", dgate, 2)
+        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        code = lib.la2_gated_norm_backward(_ptr(du), _ptr(o), _ptr(gate), sb, sl, _ptr(weight),
+                                           _ptr(do), _ptr(dgate), tb, tl, _ptr(dw), float(eps),
+                                           flags, B, H, L, e, _dt(o), _ptr(workspace), nbytes,
+                                           _stream(stream, dev))
+    _check(code, "la2_gated_norm_backward")
+    return do, dgate, dw
+
+
+def _residual_args(x, weight, post_weight, post_norm):
+    D = x.shape[-1]
+    for name, w in (("weight", weight), ("post_weight", post_weight)):
+        if w is not None and (w.dtype != torch.float32 or tuple(w.shape) != (D,)):
+            raise ValueError(f"{name} must be float32 [D]")
+    if post_weight is not None and not post_norm:
+        raise ValueError("post_weight is given but post_norm is False")
+    return D, LA2_NORM_POST if post_norm else 0
+
+
+def residual_norm(h, y=None, weight=None, *, post_norm: bool = False, post_weight=None,
+                  alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6, dtype=None, out=None,
+                  stream=None):
+    """The residual sum after a block and the norm before the next:
+    h_new = alpha h + beta p, n = h_new / sqrt(mean(h_new^2) + eps) * weight,
+    with p = y or (post_norm) y / sqrt(mean(y^2) + eps) * post_weight; rows are
+    the last axis.  y is of h's dtype, or bfloat16 with a float32 h; n is of
+    y's.  Returns (h_new, n); without y the norm of h alone, (h, n), n of
+    `dtype` (h's when None).  out: (h_new, n) to write, which may be h and y
+    themselves; without y, n."""
+    lib = library()
+    dev = _devices(("h", h), ("y", y), ("weight", weight), ("post_weight", post_weight))
+    D, flags = _residual_args(h, weight, post_weight, post_norm)
+    if y is None and (post_norm or alpha != 1.0):
+        raise ValueError("post_norm and alpha need a block output y")
+    if y is not None and (y.shape != h.shape or dtype not in (None, y.dtype)):
+        raise ValueError("y must match h's shape, and dtype y's")
+    dt = y.dtype if y is not None else (dtype or h.dtype)
+    with torch.cuda.device(dev):
+        h_new, n = (None, out) if y is None else (None, None) if out is None else out
+        if y is not None:
+            h_new = (_out(h_new, "h_new", h.shape, h.dtype, dev) if h_new is not None
+                     else torch.empty_like(h))
+        n = _out(n, "n", h.shape, dt, dev) if n is not None else torch.empty_like(h, dtype=dt)
+        code = lib.la2_residual_norm(_ptr(h), _dt(h), _ptr(y), _ptr(weight), _ptr(post_weight),
+                                     _ptr(h_new), _ptr(n), float(alpha), float(beta), float(eps),
+                                     flags, h.numel() // D if D else 0, D, _dt(n),
+                                     _stream(stream, dev))
+    _check(code, "la2_residual_norm")
+    return (h if y is None else h_new), n
+
+
+def residual_norm_backward(dn, h_new, y=None, weight=None, *, dh_new=None, post_norm: bool = False,
+                           post_weight=None, alpha: float = 1.0, beta: float = 1.0,
+                           eps: float = 1e-6, want_dy: bool = True, out=None, workspace=None,
+                           stream=None):
+    """Gradients (dh, dy, dweight, dpost_weight) of residual_norm's inputs
+    from dn and dh_new (None: zero), the gradients of n and h_new; h_new is the
+    stored sum and y (needed with post_norm only) the block's output.  dweight
+    and dpost_weight are None without their weights, dy with want_dy False (a
+    call that had no y).  out: (dh, dy) to write; dh may be dh_new itself."""
+    lib = library()
+    dev = _devices(("dn", dn), ("h_new", h_new), ("y", y), ("weight", weight), ("dh_new", dh_new),
+                   ("post_weight", post_weight), ("workspace", workspace))
+    D, flags = _residual_args(h_new, weight, post_weight, post_norm)
+    if post_norm and y is None:
+        raise ValueError("post_norm needs the block output y")
+    if dn.shape != h_new.shape or (y is not None and (y.shape != dn.shape or y.dtype != dn.dtype)):
+        raise ValueError("dn and y must match h_new's shape and have one dtype")
+    if dh_new is not None and (dh_new.shape != h_new.shape or dh_new.dtype != h_new.dtype):
+        raise ValueError("dh_new must match h_new's shape and dtype")
+    with torch.cuda.device(dev):
+        dh, dy = (None, None) if out is None else out
+        dh = (_out(dh, "dh", h_new.shape, h_new.dtype, dev) if dh is not None
+              else torch.empty_like(h_new))
+        if not want_dy:
+            dy = None
+        else:
+            dy = (_out(dy, "dy", dn.shape, dn.dtype, dev) if dy is not None
+                  else torch.empty_like(dn))
+        dw = None if weight is None else torch.empty_like(weight)
+        dpw = None if post_weight is None else torch.empty_like(post_weight)
+        N = h_new.numel() // D if D else 0
+        if workspace is None and (dw is not None or dpw is not None):
+            workspace = _workspace(
+                workspace_size(LA2_OP_RESIDUAL_NORM_BACKWARD, 1, 1, N, D, D, dn.dtype), dev)
+        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        code = lib.la2_residual_norm_backward(
+            _ptr(dn), _ptr(dh_new), _ptr(h_new), _dt(h_new), _ptr(y), _ptr(weight),
+            _ptr(post_weight), _ptr(dh), _ptr(dy), _ptr(dw), _ptr(dpw), float(alpha), float(beta),
+            float(eps), flags, N, D, _dt(dn), _ptr(workspace), nbytes, _stream(stream, dev))
+    _check(code, "la2_residual_norm_backward")
+    return dh, dy, dw, dpw
+
+
+def pool_copy(pool, src, dst, *, source=None, stream=None):
+    """States moved between slots, all at once: pool[dst[n]] = pool[src[n]] as
+    it was before the call (src[n] < 0: cleared; dst[n] < 0: no move), for
+    forking, reordering, compacting and clearing requests.  pool float32
+    [P,H,d,e], or [layers,P,H,d,e] with the same moves in every layer; src, dst
+    int32 [N], the destinations distinct.  source: another pool to copy from
+    (same layers, H, d, e; any number of slots).  Returns pool."""
+    lib = library()
+    origin = pool if source is None else source
+    dev = _devices(("pool", pool), ("source", source), ("src", src), ("dst", dst))
+    for name, t in (("pool", pool), ("source", origin)):
+        if t.dtype != torch.float32 or t.dim() not in (4, 5):
+            raise ValueError(f"{name} must be float32 [P,H,d,e] or [layers,P,H,d,e]")
+    layers = pool.shape[0] if pool.dim() == 5 else 1
+    if (origin.dim() != pool.dim() or origin.shape[-3:] != pool.shape[-3:]
+            or (pool.dim() == 5 and origin.shape[0] != layers)):
+        raise ValueError("source must match pool but for its number of slots")
+    if src.dtype != torch.int32 or src.dim() != 1 or dst.dtype != torch.int32 or dst.shape != src.shape:
+        raise ValueError("src and dst must be int32 [N]")
+    H, d, e = pool.shape[-3:]
+    with torch.cuda.device(dev):
+        code = lib.la2_pool_copy(_ptr(origin), origin.shape[-4], _ptr(pool), pool.shape[-4],
+                                 _ptr(src), _ptr(dst), src.numel(), layers, H, d, e,
+                                 _stream(stream, dev))
+    _check(code, "la2_pool_copy")
+    return pool
 
 
 def decode_step(q, k, v, lam, kv, *, out=None, stream=None):

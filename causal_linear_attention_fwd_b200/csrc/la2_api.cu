@@ -17,6 +17,9 @@
 #include "la2_decode.cuh"
 #include "la2_dlam_tc.cuh"
 #include "la2_fmap.cuh"
+#include "la2_norm.cuh"
+#include "la2_pool.cuh"
+#include "la2_rotary.cuh"
 #include "la2_shard.cuh"
 #include "la2_simt.cuh"
 #include "la2_tc.cuh"
@@ -40,7 +43,8 @@ enum KernelId {
   K_SIMT_REV_SCAN, K_SIMT_DKDV, K_DECODE, K_TC_FWD_STATE, K_TC_FWD, K_TC_DQ,
   K_TC_REV_STATE, K_TC_DV, K_TC_DK, K_SCAN_FWD, K_SCAN_REV, K_SIMT_DLAMBDA,
   K_SIMT_DLAMBDA_STATE, K_SIMT_DLAMBDA_SCAN, K_TC_DECODE_UNITS, K_FMAP, K_FMAP_GRAD, K_TC_DKDV,
-  K_TC_DLAMBDA, K_TC_DLAMBDA_STATE, K_STATE_PAD, K_COUNT
+  K_TC_DLAMBDA, K_TC_DLAMBDA_STATE, K_STATE_PAD, K_ROTARY, K_ROTARY_GRAD, K_GATED_NORM,
+  K_GATED_NORM_GRAD, K_RESIDUAL_NORM, K_RESIDUAL_NORM_GRAD, K_NORM_WEIGHT_SUM, K_POOL_COPY, K_COUNT
 };
 const char *kKernelName[K_COUNT] = {
     "simt_fwd_chunk_state", "simt_scan_fwd", "simt_fwd", "simt_dq",
@@ -48,7 +52,8 @@ const char *kKernelName[K_COUNT] = {
     "tc_fwd_chunk_state", "tc_fwd", "tc_dq", "tc_rev_chunk_state", "tc_dv", "tc_dk",
     "scan_fwd", "scan_rev", "simt_dlambda", "simt_dlambda_chunk_state", "simt_dlambda_scan",
     "tc_decode_units", "feature_map", "feature_map_grad", "tc_dkdv", "tc_dlambda",
-    "tc_dlambda_chunk_state", "state_pad"};
+    "tc_dlambda_chunk_state", "state_pad", "rotary", "rotary_grad", "gated_norm",
+    "gated_norm_grad", "residual_norm", "residual_norm_grad", "norm_weight_sum", "pool_copy"};
 
 struct ProfRec {
   int kid;
@@ -577,6 +582,343 @@ la2_status fmap_call(const void *q, const void *k, const void *gq, const void *g
 
 }  // namespace
 
+// ---------------------------------------------- norms, rotary, pool copies
+namespace {
+
+// Any byte shared by an output with an input or with another output, but for
+// an output that is exactly the input named beside it (in place).
+struct OutSpan {
+  Span s;
+  const void *over;  // the one input whose very buffer it may be, or null
+};
+bool out_overlap(std::initializer_list<OutSpan> outs, std::initializer_list<Span> ins) {
+  for (const OutSpan *o = outs.begin(); o != outs.end(); o++) {
+    for (const Span &i : ins)
+      if (overlaps(o->s, i) && !(o->over && o->over == i.p && o->s.p == i.p)) return true;
+    for (const OutSpan *q = o + 1; q != outs.end(); q++)
+      if (overlaps(o->s, q->s)) return true;
+  }
+  return false;
+}
+bool all_aligned16(std::initializer_list<const void *> ps) {
+  for (const void *p : ps)
+    if (p && !aligned16(p)) return false;
+  return true;
+}
+bool dtype_ok(la2_dtype dt) { return dt == LA2_F32 || dt == LA2_BF16; }
+
+// CTAs per SM of a kernel, looked up once per kernel.
+template <typename K>
+int resident(K kernel, int threads, size_t smem) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess ||
+      n < 1)
+    n = 1;
+  return n;
+}
+
+// Partial rows of weight gradients that a backward may write per SM: its
+// CTAs per SM, at most this many.
+constexpr int kNormGradPerSm = 4;
+constexpr int kNormMaxCols = 16384;  // widest row that one CTA holds
+
+// How a gated norm's CTAs cover the columns: see gated_kernel.
+struct GatedPlan {
+  int nt, tpr, cols, slices, rpc;
+};
+GatedPlan gated_plan(int H, int e, bool row) {
+  GatedPlan g;
+  const int D = H * e;
+  if (row) {
+    g.nt = D <= 512 ? 128 : D <= 4096 ? 256 : 512;
+    g.tpr = D <= 512 ? 32 : g.nt;
+    g.cols = D;
+    g.slices = 1;
+  } else {
+    // the most heads side by side that divide H, so no lane is idle
+    g.nt = 256;
+    int heads = g.nt * 8 / e;
+    while (H % heads) heads /= 2;
+    g.cols = heads * e;
+    g.tpr = g.cols / 8;
+    g.slices = H / heads;
+  }
+  g.rpc = g.nt / g.tpr;
+  return g;
+}
+int64_t grad_rows(int64_t rows, int rpc, int slices, int per_sm) {
+  const int64_t need = (rows + rpc - 1) / rpc;
+  const int64_t full = (int64_t)device_sms() * per_sm / slices;
+  return need < full ? need : (full > 1 ? full : 1);
+}
+
+size_t norm_ws_bytes(int op, int B, int H, int64_t L, int d, int e, la2_dtype dt) {
+  if (!dtype_ok(dt)) return 0;
+  if (op == LA2_OP_RESIDUAL_NORM_BACKWARD) {
+    if (d < 1 || d > kNormMaxCols) return 0;
+    const int64_t rows = (int64_t)B * H * L;
+    const int64_t most = (int64_t)device_sms() * kNormGradPerSm;
+    return (size_t)(rows < most ? rows : most) * d * sizeof(float) * 2;
+  }
+  if (e != 64 && e != 128) return 0;
+  const int64_t rows = (int64_t)B * L;
+  int64_t most = 0;
+  for (int row = 0; row < 2; row++) {
+    if (row && (int64_t)H * e > kNormMaxCols) continue;
+    const GatedPlan g = gated_plan(H, e, row);
+    // a weight that the heads share has `slices` rows of e per CTA row, which
+    // is never more than one row of H * e
+    const int64_t n = grad_rows(rows, g.rpc, g.slices, kNormGradPerSm) * H * e;
+    if (n > most) most = n;
+  }
+  return (size_t)most * sizeof(float);
+}
+
+cudaError_t colsum(const float *a, const float *b, float *ya, float *yb, int64_t rows, int cols,
+                   cudaStream_t st) {
+  using namespace la2::norm;
+  return timed(K_NORM_WEIGHT_SUM, st, [&] {
+    colsum_kernel<<<dim3((unsigned)((cols + kSumCols - 1) / kSumCols), yb ? 2 : 1),
+                    kSumCols * kSumRows, 0, st>>>(a, b, ya, yb, (int)rows, cols);
+  });
+}
+
+template <typename T, bool ROW, bool GRAD, int NT, int NV>
+cudaError_t gated_launch(la2::norm::Gated p, const GatedPlan &g, float *dw, cudaStream_t st) {
+  auto kern = la2::norm::gated_kernel<T, ROW, GRAD, NT, NV>;
+  const size_t smem = GRAD && p.dw ? (size_t)NT * NV * 8 * sizeof(float) : 0;
+  if (cudaError_t e = opt_in_smem(kern, smem)) return e;
+  static const int per_sm = resident(kern, NT, (size_t)(GRAD ? NT * NV * 8 * sizeof(float) : 0));
+  const int cap = GRAD && per_sm > kNormGradPerSm ? kNormGradPerSm : per_sm;
+  const int64_t rows = grad_rows(p.rows, g.rpc, g.slices, cap);
+  cudaError_t e = timed(GRAD ? K_GATED_NORM_GRAD : K_GATED_NORM, st, [&] {
+    kern<<<dim3((unsigned)rows, (unsigned)g.slices), NT, smem, st>>>(p, g.tpr, g.cols);
+  });
+  if (e != cudaSuccess || !GRAD || !dw) return e;
+  return p.shared ? colsum(p.dw, nullptr, dw, nullptr, rows * g.slices, p.e, st)
+                  : colsum(p.dw, nullptr, dw, nullptr, rows, p.H * p.e, st);
+}
+
+template <typename T, bool GRAD>
+cudaError_t gated_call(const la2::norm::Gated &p, bool row, float *dw, cudaStream_t st) {
+  const GatedPlan g = gated_plan(p.H, p.e, row);
+  if (!row) return gated_launch<T, false, GRAD, 256, 1>(p, g, dw, st);
+  if (g.nt == 128) return gated_launch<T, true, GRAD, 128, 2>(p, g, dw, st);
+  if (g.nt == 256) return gated_launch<T, true, GRAD, 256, 2>(p, g, dw, st);
+  return gated_launch<T, true, GRAD, 512, 4>(p, g, dw, st);
+}
+
+template <typename T, typename R, bool POST, bool GRAD, int V, int NT, int TPR, int NV>
+cudaError_t residual_launch(la2::norm::Residual p, float *dw, float *dpw, cudaStream_t st) {
+  constexpr int RPC = NT / TPR;
+  const int sms = device_sms();
+  const int64_t need = (p.rows + RPC - 1) / RPC;
+  if constexpr (!GRAD) {
+    auto kern = la2::norm::residual_kernel<T, R, POST, V, NT, TPR, NV>;
+    static const int per_sm = resident(kern, NT, 0);
+    const int64_t full = (int64_t)sms * per_sm;
+    return timed(K_RESIDUAL_NORM, st, [&] {
+      kern<<<(unsigned)(need < full ? need : full), NT, 0, st>>>(p);
+    });
+  } else {
+    auto kern = la2::norm::residual_grad_kernel<T, R, POST, V, NT, TPR, NV>;
+    constexpr size_t smem = (size_t)NT * NV * V * sizeof(float) * (POST ? 2 : 1);
+    if (cudaError_t e = opt_in_smem(kern, smem)) return e;
+    static const int per_sm = resident(kern, NT, smem);
+    const int64_t full = (int64_t)sms * (per_sm < kNormGradPerSm ? per_sm : kNormGradPerSm);
+    const int64_t rows = need < full ? need : full;
+    if (dpw) p.dpw = p.dw + rows * p.D;
+    if (!dw) p.dw = nullptr;
+    cudaError_t e = timed(K_RESIDUAL_NORM_GRAD, st, [&] { kern<<<(unsigned)rows, NT, smem, st>>>(p); });
+    if (e != cudaSuccess || (!dw && !dpw)) return e;
+    return colsum(p.dw, p.dpw, dw, dpw, rows, p.D, st);
+  }
+}
+
+// Rows of whole 16-byte pieces (D a multiple of 8) move as vectors: a warp
+// per row up to 512 columns, else a CTA per row; other widths value by value.
+template <typename T, typename R, bool POST, bool GRAD>
+cudaError_t residual_shape(const la2::norm::Residual &p, float *dw, float *dpw, cudaStream_t st) {
+  if (p.D % 8 == 0) {
+    if (p.D <= 512) return residual_launch<T, R, POST, GRAD, 8, 128, 32, 2>(p, dw, dpw, st);
+    if (p.D <= 4096) return residual_launch<T, R, POST, GRAD, 8, 256, 256, 2>(p, dw, dpw, st);
+    return residual_launch<T, R, POST, GRAD, 8, 512, 512, 4>(p, dw, dpw, st);
+  }
+  if (p.D <= 2048) return residual_launch<T, R, POST, GRAD, 1, 256, 256, 8>(p, dw, dpw, st);
+  return residual_launch<T, R, POST, GRAD, 1, 1024, 1024, 16>(p, dw, dpw, st);
+}
+
+template <bool GRAD>
+cudaError_t residual_call(const la2::norm::Residual &p, la2_dtype h_dt, la2_dtype dt, bool post,
+                          float *dw, float *dpw, cudaStream_t st) {
+  using bf16 = __nv_bfloat16;
+  if (dt == LA2_F32)
+    return post ? residual_shape<float, float, true, GRAD>(p, dw, dpw, st)
+                : residual_shape<float, float, false, GRAD>(p, dw, dpw, st);
+  if (h_dt == LA2_F32)
+    return post ? residual_shape<bf16, float, true, GRAD>(p, dw, dpw, st)
+                : residual_shape<bf16, float, false, GRAD>(p, dw, dpw, st);
+  return post ? residual_shape<bf16, bf16, true, GRAD>(p, dw, dpw, st)
+              : residual_shape<bf16, bf16, false, GRAD>(p, dw, dpw, st);
+}
+
+// ------------------------------------------------------------- rotary
+// Bytes from the first to past the last value of a strided tensor.
+size_t heads_span(const la2_heads &x, int B, int n, int64_t L, int width, size_t es) {
+  return ((size_t)(B - 1) * x.batch + (size_t)(n - 1) * x.head + (size_t)(L - 1) * x.row + width) * es;
+}
+// Whether values placed with these strides, `inner` of them side by side, are
+// at places of their own: each stride steps over all that the smaller ones
+// span.
+struct Axis {
+  int64_t stride, size;
+};
+bool distinct(std::initializer_list<Axis> axes, int64_t inner) {
+  Axis a[3];
+  int n = 0;
+  for (const Axis &x : axes)
+    if (x.size > 1) a[n++] = x;
+  for (int i = 0; i < n; i++)
+    for (int j = i + 1; j < n; j++)
+      if (a[j].stride < a[i].stride) {
+        const Axis s = a[i];
+        a[i] = a[j];
+        a[j] = s;
+      }
+  for (int i = 0; i < n; i++) {
+    if (a[i].stride < inner) return false;
+    inner += a[i].stride * (a[i].size - 1);
+  }
+  return true;
+}
+// Whether two strided outputs share no value: apart in memory, or slices of
+// one buffer side by side in each row (all heads of one, then all of the
+// other) or in each head.
+bool apart(const la2_heads &x, int nx, int wx, const la2_heads &y, int ny, int wy, int B, int64_t L,
+           size_t es) {
+  const uintptr_t px = reinterpret_cast<uintptr_t>(x.p), py = reinterpret_cast<uintptr_t>(y.p);
+  if (!overlaps({x.p, heads_span(x, B, nx, L, wx, es)}, {y.p, heads_span(y, B, ny, L, wy, es)}))
+    return true;
+  if ((B > 1 && x.batch != y.batch) || (L > 1 && x.row != y.row)) return false;
+  const uintptr_t lo = px < py ? px : py;
+  if ((px - lo) % es || (py - lo) % es) return false;
+  const int64_t ox = (int64_t)((px - lo) / es), oy = (int64_t)((py - lo) / es);
+  // n: values that one tensor spans within a unit (a row's heads, or a head)
+  auto side_by_side = [&](int64_t spanx, int64_t spany, std::initializer_list<Axis> axes) {
+    if (ox < oy ? ox + spanx > oy : oy + spany > ox) return false;
+    const int64_t ex = ox + spanx, ey = oy + spany;
+    return distinct(axes, ex > ey ? ex : ey);
+  };
+  if (side_by_side((nx - 1) * x.head + wx, (ny - 1) * y.head + wy, {{x.batch, B}, {x.row, L}}))
+    return true;
+  const int n = nx > ny ? nx : ny;
+  if (nx > 1 && ny > 1 && x.head != y.head) return false;
+  return side_by_side(wx, wy, {{x.batch, B}, {x.row, L}, {nx > 1 ? x.head : y.head, n}});
+}
+
+template <bool GRAD>
+la2_status rotary_call(const la2_heads *q, const la2_heads *k, const la2_heads *v,
+                       const double *inv_freq, const int64_t *positions, int kind, void *mq,
+                       void *mk, void *mv, float scale, unsigned flags, int B, int H, int Hk,
+                       int64_t L, int d, int e, int r, la2_dtype dt, cudaStream_t stream) {
+  if (B < 0 || H < 0 || Hk < 0 || L < 0 || r < 2 || r > d || r % 2) return LA2_ERR_INVALID;
+  if (flags & ~(unsigned)LA2_ROTARY_INTERLEAVED) return LA2_ERR_INVALID;
+  if (kind < LA2_POSITIONS_ROW || kind > LA2_POSITIONS_TABLE) return LA2_ERR_INVALID;
+  if (!shape_supported(d, v ? e : d, dt)) return LA2_ERR_UNSUPPORTED;
+  if (Hk == 0 ? H != 0 : H % Hk) return LA2_ERR_INVALID;
+  if ((int64_t)B * H * L == 0) return LA2_OK;
+  if (!q || !k || !q->p || !k->p || (v && !v->p) || !mq || !mk || !inv_freq ||
+      (v != nullptr) != (mv != nullptr) || (kind != LA2_POSITIONS_ROW) != (positions != nullptr))
+    return LA2_ERR_INVALID;
+  if (!all_aligned16({mq, mk, mv}) || reinterpret_cast<uintptr_t>(inv_freq) % 8 ||
+      reinterpret_cast<uintptr_t>(positions) % 8)
+    return LA2_ERR_INVALID;
+  const size_t es = esize(dt);
+  const la2_heads *in[3] = {q, k, v};
+  void *major[3] = {mq, mk, mv};
+  const int n[3] = {H, Hk, Hk}, width[3] = {d, d, e}, parts = v ? 3 : 2;
+  bool vec = r % 16 == 0;
+  Span strided[3] = {{nullptr, 0}, {nullptr, 0}, {nullptr, 0}}, out[3] = {strided[0], strided[0], strided[0]};
+  la2::rot::Args a{};
+  for (int i = 0; i < parts; i++) {
+    const la2_heads &x = *in[i];
+    if (x.batch < 0 || x.head < 0 || x.row < 0) return LA2_ERR_INVALID;
+    if (reinterpret_cast<uintptr_t>(x.p) % es) return LA2_ERR_INVALID;
+    if (GRAD && !distinct({{x.batch, B}, {x.head, n[i]}, {x.row, L}}, width[i])) return LA2_ERR_INVALID;
+    strided[i] = {x.p, heads_span(x, B, n[i], L, width[i], es)};
+    out[i] = {major[i], (size_t)B * H * L * width[i] * es};
+    const int64_t odd = (B > 1 ? x.batch : 0) | (n[i] > 1 ? x.head : 0) | (L > 1 ? x.row : 0);
+    vec = vec && aligned16(x.p) && (odd * (int64_t)es) % 16 == 0;
+    a.part[i] = {x.p, major[i], x.batch, x.head, x.row, n[i], width[i], i < 2 ? r : 0};
+  }
+  const Span pos = {positions, kind == LA2_POSITIONS_START   ? (size_t)B * 8
+                               : kind == LA2_POSITIONS_TABLE ? (size_t)B * L * 8
+                                                             : 0};
+  const Span freq = {inv_freq, (size_t)r / 2 * 8};
+  if (!GRAD) {
+    if (out_overlap({{out[0], nullptr}, {out[1], nullptr}, {out[2], nullptr}},
+                    {strided[0], strided[1], strided[2], pos, freq}))
+      return LA2_ERR_INVALID;
+  } else {
+    for (int i = 0; i < parts; i++) {
+      if (out_overlap({{strided[i], nullptr}}, {out[0], out[1], out[2], pos, freq})) return LA2_ERR_INVALID;
+      for (int j = i + 1; j < parts; j++)
+        if (!apart(*in[i], n[i], width[i], *in[j], n[j], width[j], B, L, es)) return LA2_ERR_INVALID;
+    }
+  }
+  a.parts = parts;
+  a.freq = inv_freq;
+  a.pos = positions;
+  a.pos_mode = kind;
+  a.L = L;
+  a.rows = (int64_t)B * L;
+  a.rep = H / Hk;
+  a.r = r;
+  a.inter = (flags & LA2_ROTARY_INTERLEAVED) != 0;
+  a.scale = scale;
+  using namespace la2::rot;
+  const int64_t tiles = (a.rows + TOK - 1) / TOK;
+  if (tiles > INT32_MAX) return LA2_ERR_UNSUPPORTED;
+  // few tokens (decode): the heads of a token are spread over several CTAs
+  const int per = LANES / (d / (vec ? 16 : 2));
+  const int64_t groups = (H + per - 1) / per, want = (4 * (int64_t)device_sms() + tiles - 1) / tiles;
+  const dim3 grid((unsigned)tiles, (unsigned)(want < groups ? want : groups));
+  const size_t smem = (size_t)TOK * (r / 2) * sizeof(float2);
+  return to_status(timed(GRAD ? K_ROTARY_GRAD : K_ROTARY, stream, [&] {
+    if (dt == LA2_F32) {
+      if (vec) rotary_kernel<float, GRAD, 8><<<grid, NT, smem, stream>>>(a);
+      else rotary_kernel<float, GRAD, 1><<<grid, NT, smem, stream>>>(a);
+    } else {
+      if (vec) rotary_kernel<__nv_bfloat16, GRAD, 8><<<grid, NT, smem, stream>>>(a);
+      else rotary_kernel<__nv_bfloat16, GRAD, 1><<<grid, NT, smem, stream>>>(a);
+    }
+  }));
+}
+
+// The checks that both directions of the gated norm share.  LA2_OK with
+// *empty: nothing to do.
+la2_status gated_checks(unsigned flags, int B, int H, int64_t L, int e, float eps, la2_dtype dt,
+                        const void *gate, int64_t gate_batch, int64_t gate_row, bool *empty) {
+  *empty = false;
+  if (B < 0 || H < 0 || L < 0 || !(eps > 0.f) || gate_batch < 0 || gate_row < 0) return LA2_ERR_INVALID;
+  if (flags & ~(unsigned)(LA2_NORM_SILU | LA2_NORM_ROW | LA2_NORM_SHARED_WEIGHT)) return LA2_ERR_INVALID;
+  if ((flags & LA2_NORM_ROW) && (flags & LA2_NORM_SHARED_WEIGHT)) return LA2_ERR_INVALID;
+  if (!dtype_ok(dt) || (e != 64 && e != 128)) return LA2_ERR_UNSUPPORTED;
+  if ((flags & LA2_NORM_ROW) && (int64_t)H * e > kNormMaxCols) return LA2_ERR_UNSUPPORTED;
+  if ((int64_t)H * e > INT32_MAX) return LA2_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(gate) % esize(dt)) return LA2_ERR_INVALID;
+  *empty = (int64_t)B * H * L == 0;
+  return LA2_OK;
+}
+size_t rows_span(int64_t sb, int64_t sl, int B, int64_t L, int64_t D, size_t es) {
+  return ((size_t)(B - 1) * sb + (size_t)(L - 1) * sl + D) * es;
+}
+bool rows_vec(const void *p, int64_t sb, int64_t sl, int B, int64_t L, size_t es) {
+  return aligned16(p) && (((B > 1 ? sb : 0) | (L > 1 ? sl : 0)) * (int64_t)es) % 16 == 0;
+}
+
+}  // namespace
+
 extern "C" {
 
 const char *la2_status_string(la2_status s) {
@@ -605,7 +947,10 @@ int la2_set_option(int option, int value) {
 }
 
 size_t la2_workspace_size(int op, int B, int H, int64_t L, int d, int e, la2_dtype dt) {
-  if (B <= 0 || H <= 0 || L <= 0 || !shape_supported(d, e, dt)) return 0;
+  if (B <= 0 || H <= 0 || L <= 0) return 0;
+  if (op == LA2_OP_GATED_NORM_BACKWARD || op == LA2_OP_RESIDUAL_NORM_BACKWARD)
+    return norm_ws_bytes(op, B, H, L, d, e, dt);
+  if (!shape_supported(d, e, dt)) return 0;
   if (op == LA2_OP_DLAMBDA) {
     const Path p = choose_path(d, e, dt);
     if (p == PATH_NONE) return 0;
@@ -1213,6 +1558,215 @@ la2_status la2_feature_map_backward(const void *q, const void *k, const void *dp
                                     const void *dphi_k, void *dq, void *dk, int64_t n,
                                     la2_dtype dt, cudaStream_t stream) {
   return fmap_call<true>(q, k, dphi_q, dphi_k, dq, dk, n, dt, stream);
+}
+
+la2_status la2_rotary(const la2_heads *q, const la2_heads *k, const la2_heads *v,
+                      const double *inv_freq, const int64_t *positions, int positions_kind,
+                      void *rq, void *rk, void *rv, float scale, unsigned flags, int B, int H,
+                      int Hk, int64_t L, int d, int e, int r, la2_dtype dt, cudaStream_t stream) {
+  return rotary_call<false>(q, k, v, inv_freq, positions, positions_kind, rq, rk, rv, scale, flags,
+                            B, H, Hk, L, d, e, r, dt, stream);
+}
+
+la2_status la2_rotary_backward(const void *dq, const void *dk, const void *dv,
+                               const double *inv_freq, const int64_t *positions,
+                               int positions_kind, const la2_heads *gq, const la2_heads *gk,
+                               const la2_heads *gv, float scale, unsigned flags, int B, int H,
+                               int Hk, int64_t L, int d, int e, int r, la2_dtype dt,
+                               cudaStream_t stream) {
+  return rotary_call<true>(gq, gk, gv, inv_freq, positions, positions_kind, const_cast<void *>(dq),
+                           const_cast<void *>(dk), const_cast<void *>(dv), scale, flags, B, H, Hk,
+                           L, d, e, r, dt, stream);
+}
+
+la2_status la2_gated_norm(const void *o, const void *gate, int64_t gate_batch, int64_t gate_row,
+                          const float *weight, void *u, float eps, unsigned flags, int B, int H,
+                          int64_t L, int e, la2_dtype dt, cudaStream_t stream) {
+  bool empty;
+  la2_status s = gated_checks(flags, B, H, L, e, eps, dt, gate, gate_batch, gate_row, &empty);
+  if (s != LA2_OK || empty) return s;
+  if (!o || !u || !all_aligned16({o, u, weight})) return LA2_ERR_INVALID;
+  const size_t es = esize(dt), n = (size_t)B * H * L * e * es;
+  const int64_t D = (int64_t)H * e;
+  const size_t nw = (size_t)(flags & LA2_NORM_SHARED_WEIGHT ? e : D) * 4;
+  if (out_overlap({{{u, n}, nullptr}},
+                  {{o, n}, {gate, rows_span(gate_batch, gate_row, B, L, D, es)}, {weight, nw}}))
+    return LA2_ERR_INVALID;
+  la2::norm::Gated p{};
+  p.o = o;
+  p.gate = gate;
+  p.u = u;
+  p.weight = weight;
+  p.gate_b = gate_batch;
+  p.gate_l = gate_row;
+  p.L = L;
+  p.rows = (int64_t)B * L;
+  p.H = H;
+  p.e = e;
+  p.silu = (flags & LA2_NORM_SILU) != 0;
+  p.shared = (flags & LA2_NORM_SHARED_WEIGHT) != 0;
+  p.gate_vec = rows_vec(gate, gate_batch, gate_row, B, L, es);
+  p.eps = eps;
+  const bool row = (flags & LA2_NORM_ROW) != 0;
+  return to_status(dt == LA2_F32 ? gated_call<float, false>(p, row, nullptr, stream)
+                                 : gated_call<__nv_bfloat16, false>(p, row, nullptr, stream));
+}
+
+la2_status la2_gated_norm_backward(const void *du, const void *o, const void *gate,
+                                   int64_t gate_batch, int64_t gate_row, const float *weight,
+                                   void *d_o, void *dgate, int64_t dgate_batch, int64_t dgate_row,
+                                   float *dweight, float eps, unsigned flags, int B, int H,
+                                   int64_t L, int e, la2_dtype dt, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t stream) {
+  bool empty;
+  la2_status s = gated_checks(flags, B, H, L, e, eps, dt, gate, gate_batch, gate_row, &empty);
+  if (s != LA2_OK) return s;
+  if (dgate_batch < 0 || dgate_row < 0) return LA2_ERR_INVALID;
+  const size_t es = esize(dt), n = (size_t)B * H * L * e * es;
+  const int64_t D = (int64_t)H * e;
+  const size_t nw = (size_t)(flags & LA2_NORM_SHARED_WEIGHT ? e : D) * 4;
+  if (!all_aligned16({du, o, weight, d_o, dweight, workspace}) ||
+      reinterpret_cast<uintptr_t>(dgate) % es)
+    return LA2_ERR_INVALID;
+  if (empty) return dweight ? to_status(cudaMemsetAsync(dweight, 0, nw, stream)) : LA2_OK;
+  if (!du || !o || !d_o || (gate != nullptr) != (dgate != nullptr)) return LA2_ERR_INVALID;
+  const size_t need = dweight ? norm_ws_bytes(LA2_OP_GATED_NORM_BACKWARD, B, H, L, e, e, dt) : 0;
+  if (need && (!workspace || workspace_bytes < need)) return LA2_ERR_INVALID;
+  if (dgate && !distinct({{dgate_batch, B}, {dgate_row, L}}, D)) return LA2_ERR_INVALID;
+  const Span sg = {gate, gate ? rows_span(gate_batch, gate_row, B, L, D, es) : 0};
+  const Span sd = {dgate, dgate ? rows_span(dgate_batch, dgate_row, B, L, D, es) : 0};
+  if (out_overlap({{{d_o, n}, nullptr}, {sd, nullptr}, {{dweight, nw}, nullptr},
+                   {{workspace, need}, nullptr}},
+                  {{du, n}, {o, n}, sg, {weight, nw}}))
+    return LA2_ERR_INVALID;
+  la2::norm::Gated p{};
+  p.o = o;
+  p.gate = gate;
+  p.du = du;
+  p.d_o = d_o;
+  p.dgate = dgate;
+  p.weight = weight;
+  p.dw = dweight ? static_cast<float *>(workspace) : nullptr;
+  p.gate_b = gate_batch;
+  p.gate_l = gate_row;
+  p.dgate_b = dgate_batch;
+  p.dgate_l = dgate_row;
+  p.L = L;
+  p.rows = (int64_t)B * L;
+  p.H = H;
+  p.e = e;
+  p.silu = (flags & LA2_NORM_SILU) != 0;
+  p.shared = (flags & LA2_NORM_SHARED_WEIGHT) != 0;
+  p.gate_vec = rows_vec(gate, gate_batch, gate_row, B, L, es);
+  p.dgate_vec = rows_vec(dgate, dgate_batch, dgate_row, B, L, es);
+  p.eps = eps;
+  const bool row = (flags & LA2_NORM_ROW) != 0;
+  return to_status(dt == LA2_F32 ? gated_call<float, true>(p, row, dweight, stream)
+                                 : gated_call<__nv_bfloat16, true>(p, row, dweight, stream));
+}
+
+la2_status la2_residual_norm(const void *h, la2_dtype h_dt, const void *y, const float *weight,
+                             const float *post_weight, void *h_new, void *n, float alpha,
+                             float beta, float eps, unsigned flags, int64_t N, int D,
+                             la2_dtype dt, cudaStream_t stream) {
+  if (N < 0 || D < 1 || !(eps > 0.f) || (flags & ~(unsigned)LA2_NORM_POST)) return LA2_ERR_INVALID;
+  if (!dtype_ok(dt) || !dtype_ok(h_dt) || (h_dt == LA2_BF16 && dt == LA2_F32) || D > kNormMaxCols)
+    return LA2_ERR_UNSUPPORTED;
+  const bool post = (flags & LA2_NORM_POST) != 0;
+  if (post && !y) return LA2_ERR_INVALID;
+  if (N == 0) return LA2_OK;
+  if (!h || !n || (y != nullptr) != (h_new != nullptr) || (post_weight && !post)) return LA2_ERR_INVALID;
+  if (!all_aligned16({h, y, weight, post_weight, h_new, n})) return LA2_ERR_INVALID;
+  const size_t bh = (size_t)N * D * esize(h_dt), by = (size_t)N * D * esize(dt), bw = (size_t)D * 4;
+  if (out_overlap({{{h_new, bh}, h}, {{n, by}, y}},
+                  {{h, bh}, {y, y ? by : 0}, {weight, bw}, {post_weight, bw}}))
+    return LA2_ERR_INVALID;
+  la2::norm::Residual p{};
+  p.h = h;
+  p.y = y;
+  p.h_new = h_new;
+  p.n = n;
+  p.weight = weight;
+  p.post_weight = post_weight;
+  p.rows = N;
+  p.D = D;
+  p.alpha = alpha;
+  p.beta = beta;
+  p.eps = eps;
+  return to_status(residual_call<false>(p, h_dt, dt, post, nullptr, nullptr, stream));
+}
+
+la2_status la2_residual_norm_backward(const void *dn, const void *dh_new, const void *h_new,
+                                      la2_dtype h_dt, const void *y, const float *weight,
+                                      const float *post_weight, void *dh, void *dy,
+                                      float *dweight, float *dpost_weight, float alpha,
+                                      float beta, float eps, unsigned flags, int64_t N, int D,
+                                      la2_dtype dt, void *workspace, size_t workspace_bytes,
+                                      cudaStream_t stream) {
+  if (N < 0 || D < 1 || !(eps > 0.f) || (flags & ~(unsigned)LA2_NORM_POST)) return LA2_ERR_INVALID;
+  if (!dtype_ok(dt) || !dtype_ok(h_dt) || (h_dt == LA2_BF16 && dt == LA2_F32) || D > kNormMaxCols)
+    return LA2_ERR_UNSUPPORTED;
+  const bool post = (flags & LA2_NORM_POST) != 0;
+  if (!post && (post_weight || dpost_weight)) return LA2_ERR_INVALID;
+  const size_t bh = (size_t)N * D * esize(h_dt), by = (size_t)N * D * esize(dt), bw = (size_t)D * 4;
+  if (!all_aligned16({dn, dh_new, h_new, y, weight, post_weight, dh, dy, dweight, dpost_weight, workspace}))
+    return LA2_ERR_INVALID;
+  if (N == 0) {
+    cudaError_t e = cudaSuccess;
+    if (dweight) e = cudaMemsetAsync(dweight, 0, bw, stream);
+    if (e == cudaSuccess && dpost_weight) e = cudaMemsetAsync(dpost_weight, 0, bw, stream);
+    return to_status(e);
+  }
+  if (!dn || !h_new || !dh || (post && !y)) return LA2_ERR_INVALID;
+  const size_t need =
+      dweight || dpost_weight
+          ? norm_ws_bytes(LA2_OP_RESIDUAL_NORM_BACKWARD, 1, 1, N, D, D, dt)
+          : 0;
+  if (need && (!workspace || workspace_bytes < need)) return LA2_ERR_INVALID;
+  if (out_overlap({{{dh, bh}, dh_new}, {{dy, dy ? by : 0}, nullptr}, {{dweight, bw}, nullptr},
+                   {{dpost_weight, bw}, nullptr}, {{workspace, need}, nullptr}},
+                  {{dn, by}, {dh_new, bh}, {h_new, bh}, {post ? y : nullptr, by}, {weight, bw},
+                   {post_weight, bw}}))
+    return LA2_ERR_INVALID;
+  la2::norm::Residual p{};
+  p.h = h_new;
+  p.y = y;
+  p.dn = dn;
+  p.dh_new = dh_new;
+  p.dh = dh;
+  p.dy = dy;
+  p.weight = weight;
+  p.post_weight = post_weight;
+  p.dw = static_cast<float *>(workspace);
+  p.rows = N;
+  p.D = D;
+  p.alpha = alpha;
+  p.beta = beta;
+  p.eps = eps;
+  return to_status(residual_call<true>(p, h_dt, dt, post, dweight, dpost_weight, stream));
+}
+
+la2_status la2_pool_copy(const float *from, int from_size, float *to, int to_size,
+                         const int32_t *src, const int32_t *dst, int N, int layers, int H, int d,
+                         int e, cudaStream_t stream) {
+  if (N < 0 || layers < 0 || H < 0 || from_size < 0 || to_size < 0) return LA2_ERR_INVALID;
+  if (!shape_supported(d, e, LA2_F32) || N > la2::pool::MAX_MOVES) return LA2_ERR_UNSUPPORTED;
+  if (N == 0 || layers == 0 || H == 0) return LA2_OK;
+  if (!from || !to || !src || !dst || !all_aligned16({from, to}) ||
+      reinterpret_cast<uintptr_t>(src) % 4 || reinterpret_cast<uintptr_t>(dst) % 4)
+    return LA2_ERR_INVALID;
+  const int64_t bytes = (int64_t)H * d * e * sizeof(float);
+  const size_t nf = (size_t)layers * from_size * bytes, nt = (size_t)layers * to_size * bytes;
+  if (from == to && from_size != to_size) return LA2_ERR_INVALID;
+  if (out_overlap({{{to, nt}, from}}, {{from, nf}, {src, (size_t)N * 4}, {dst, (size_t)N * 4}}))
+    return LA2_ERR_INVALID;
+  auto kern = la2::pool::copy_kernel;
+  if (cudaError_t er = opt_in_smem(kern, la2::pool::SMEM)) return to_status(er);
+  return to_status(timed(K_POOL_COPY, stream, [&] {
+    kern<<<(unsigned)device_sms(), la2::pool::NT, la2::pool::SMEM, stream>>>(
+        reinterpret_cast<const char *>(from), reinterpret_cast<char *>(to), src, dst, N, from_size,
+        to_size, layers, bytes);
+  }));
 }
 
 la2_status la2_decode_tokens(const void *q, const void *k, const void *v, const float *lambda,

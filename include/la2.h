@@ -82,7 +82,8 @@ typedef enum {
 typedef enum { LA2_F32 = 0, LA2_BF16 = 1 } la2_dtype;
 
 /* Operation codes for la2_workspace_size(). */
-enum { LA2_OP_FORWARD = 0, LA2_OP_BACKWARD = 1, LA2_OP_SHARD_STATE = 2, LA2_OP_DLAMBDA = 3 };
+enum { LA2_OP_FORWARD = 0, LA2_OP_BACKWARD = 1, LA2_OP_SHARD_STATE = 2, LA2_OP_DLAMBDA = 3,
+       LA2_OP_GATED_NORM_BACKWARD = 4, LA2_OP_RESIDUAL_NORM_BACKWARD = 5 };
 
 /*
  * Bytes of device scratch that la2_forward (op = LA2_OP_FORWARD),
@@ -93,6 +94,10 @@ enum { LA2_OP_FORWARD = 0, LA2_OP_BACKWARD = 1, LA2_OP_SHARD_STATE = 2, LA2_OP_D
  * sequence chunks that run in parallel (the split of one long sequence over
  * several CTAs); it may be 0 when the sequence is not split.  Returns 0 for
  * unsupported arguments as well; the call then reports the error.
+ * LA2_OP_GATED_NORM_BACKWARD takes B, H, L, e of la2_gated_norm_backward (d is
+ * ignored; the size covers both kinds of norm); LA2_OP_RESIDUAL_NORM_BACKWARD
+ * takes the rows as B * H * L and their width as d (e is ignored).  Their
+ * scratch holds partial sums of the weights' gradients.
  */
 size_t la2_workspace_size(int op, int B, int H, int64_t L, int d, int e,
                           la2_dtype dt);
@@ -306,6 +311,134 @@ la2_status la2_feature_map_backward(const void *q, const void *k, const void *dp
                                     la2_dtype dt, cudaStream_t stream);
 
 /*
+ * Rotary positions, between a layer's fused projection and the attention.
+ *
+ * A tensor on the projection's side is described by la2_heads: its first
+ * value and the strides, in values, of its batch, head and row (the columns
+ * of a head are contiguous; strides >= 0; the pointer needs its element's
+ * alignment only).  A token-major projection [B, L, W] has batch = L * W,
+ * row = W, head = d.
+ *
+ * la2_rotary: q [B,H,L,d], k [B,Hk,L,d] and, unless NULL, v [B,Hk,L,e] (strided;
+ * Hk divides H: k and v heads shared by H / Hk neighbouring q heads) to rq, rk
+ * [B,H,L,d] and rv [B,H,L,e], contiguous as the attention calls take them, a
+ * shared head repeated for each of its q heads.  Pair i = 0..r/2-1 of the
+ * first r columns of each q and k head (r even, 2 <= r <= d) turns by the
+ * angle p * inv_freq[i] of its row's position p:
+ *     a' = scale (a cos - b sin),   b' = scale (a sin + b cos)
+ * with (a, b) = columns (i, i + r/2), or (2i, 2i + 1) with flag
+ * LA2_ROTARY_INTERLEAVED; the other columns, and v, are copied.  inv_freq is
+ * fp64 [r/2]; the angle is formed in fp64, so positions far into a text keep
+ * their digits.  positions (int64) by positions_kind: LA2_POSITIONS_ROW (NULL)
+ * p = row; LA2_POSITIONS_START [B]: p = positions[b] + row (a request that goes
+ * on); LA2_POSITIONS_TABLE [B,L]: p = positions[b][row] (packed documents).
+ *
+ * la2_rotary_backward: the chain rule.  dq, dk [B,H,L,d], dv [B,H,L,e]
+ * (contiguous, as la2_backward writes them) to gq, gk, gv of q's, k's and v's
+ * shapes, written through their strides: the copies of a shared head are added
+ * (fp32, in the order of the heads), pairs turn by the opposite angle times
+ * scale.  gq, gk and gv may be slices of one buffer (side by side in each row
+ * or each head); otherwise no two values may share a place.
+ *
+ * Arithmetic in fp32, one rounding to dt.  An output may share no byte with an
+ * input.  B, H or L = 0: nothing is launched.  Errors: LA2_ERR_INVALID for
+ * negative sizes or strides, an odd r or one outside 2..d, H not a multiple of
+ * Hk, unknown flags or kinds, a NULL or misaligned pointer (contiguous tensors:
+ * 16 bytes; inv_freq, positions: 8), an overlap; LA2_ERR_UNSUPPORTED for
+ * another dt, d or e.  The pages give linear attention no positions; the
+ * rotation is the standard one, and the layouts are this library's.
+ */
+typedef struct {
+    void *p;
+    int64_t batch, head, row;
+} la2_heads;
+enum { LA2_ROTARY_INTERLEAVED = 1 };
+enum { LA2_POSITIONS_ROW = 0, LA2_POSITIONS_START = 1, LA2_POSITIONS_TABLE = 2 };
+la2_status la2_rotary(const la2_heads *q, const la2_heads *k, const la2_heads *v,
+                      const double *inv_freq, const int64_t *positions, int positions_kind,
+                      void *rq, void *rk, void *rv, float scale, unsigned flags, int B, int H,
+                      int Hk, int64_t L, int d, int e, int r, la2_dtype dt, cudaStream_t stream);
+la2_status la2_rotary_backward(const void *dq, const void *dk, const void *dv,
+                               const double *inv_freq, const int64_t *positions,
+                               int positions_kind, const la2_heads *gq, const la2_heads *gk,
+                               const la2_heads *gv, float scale, unsigned flags, int B, int H,
+                               int Hk, int64_t L, int d, int e, int r, la2_dtype dt,
+                               cudaStream_t stream);
+
+/*
+ * Norm of the attention's output, gated, for the output projection:
+ *     u = o / sqrt(mean(o^2) + eps) * weight * a(gate)
+ * o [B,H,L,e] as the attention writes it, u [B,L,H*e] token-major.  The mean
+ * runs over each head's e columns, or with LA2_NORM_ROW over the token's
+ * H * e.  weight fp32 [H*e], or [e] for every head alike with
+ * LA2_NORM_SHARED_WEIGHT (not with LA2_NORM_ROW), or NULL (ones).  gate
+ * [B,L,H*e] with the given strides (in values) of its batch and row, or NULL
+ * (no gate); a(x) is the sigmoid, or x * sigmoid(x) with LA2_NORM_SILU.
+ *
+ * la2_gated_norm_backward: from du (of u's shape) the gradients d_o (of o's),
+ * dgate (of gate's, through its own strides; NULL exactly when gate is) and,
+ * unless NULL, dweight (fp32, of weight's shape, written; the sum over tokens
+ * is made in a fixed order).  With dweight it needs a workspace of
+ * la2_workspace_size(LA2_OP_GATED_NORM_BACKWARD, ...) bytes.
+ *
+ * A row of zeros has u = 0.  Arithmetic in fp32, one rounding to dt.  Errors:
+ * LA2_ERR_INVALID for negative sizes or strides, eps not above 0, unknown
+ * flags, a NULL or misaligned pointer (16 bytes; gate and dgate: their
+ * element), a workspace that is missing or too small, an output sharing bytes
+ * with any other argument or (dgate) with itself; LA2_ERR_UNSUPPORTED for
+ * another dt or e, or LA2_NORM_ROW with H * e above 16,384.  B, H or L = 0:
+ * only dweight is written (zeros).
+ */
+enum { LA2_NORM_SILU = 1, LA2_NORM_ROW = 2, LA2_NORM_SHARED_WEIGHT = 4, LA2_NORM_POST = 8 };
+la2_status la2_gated_norm(const void *o, const void *gate, int64_t gate_batch, int64_t gate_row,
+                          const float *weight, void *u, float eps, unsigned flags, int B, int H,
+                          int64_t L, int e, la2_dtype dt, cudaStream_t stream);
+la2_status la2_gated_norm_backward(const void *du, const void *o, const void *gate,
+                                   int64_t gate_batch, int64_t gate_row, const float *weight,
+                                   void *d_o, void *dgate, int64_t dgate_batch, int64_t dgate_row,
+                                   float *dweight, float eps, unsigned flags, int B, int H,
+                                   int64_t L, int e, la2_dtype dt, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The residual sum after a block and the norm before the next one:
+ *     h_new = alpha h + beta p,   n = h_new / sqrt(mean(h_new^2) + eps) * weight
+ * with p = y, the block's output, or with LA2_NORM_POST
+ * p = y / sqrt(mean(y^2) + eps) * post_weight.  All [N, D] contiguous; h and
+ * h_new of type h_dt, y and n of type dt (h_dt = dt, or LA2_F32 with dt =
+ * LA2_BF16); weights fp32 [D] or NULL (ones).  n comes from the sum before it
+ * is rounded to h_dt.  y and h_new both NULL: n is the norm of h (alpha, beta
+ * unused).  In place: h_new may be the very buffer of h, n that of y.
+ *
+ * la2_residual_norm_backward: from dn (of n's shape and type) and dh_new (of
+ * h_new's; NULL: zero), with h_new as stored, the gradients dh (h_dt) and,
+ * unless NULL, dy (dt), dweight and dpost_weight (fp32 [D], written, summed in
+ * a fixed order).  y is read with LA2_NORM_POST only.  With either weight's
+ * gradient it needs a workspace of
+ * la2_workspace_size(LA2_OP_RESIDUAL_NORM_BACKWARD, 1, 1, N, D, D, dt) bytes.
+ * dh may be the very buffer of dh_new.  After a call without y, pass alpha =
+ * 1 and dy NULL.
+ *
+ * Arithmetic in fp32, one rounding per output.  Errors: LA2_ERR_INVALID for
+ * N < 0, D < 1, eps not above 0, unknown flags, a NULL or misaligned pointer
+ * (16 bytes), post_weight or dpost_weight without LA2_NORM_POST, a missing or
+ * small workspace, an overlap other than the in-place ones;
+ * LA2_ERR_UNSUPPORTED for other types or D above 16,384.  N = 0: only the
+ * weights' gradients are written (zeros).
+ */
+la2_status la2_residual_norm(const void *h, la2_dtype h_dt, const void *y, const float *weight,
+                             const float *post_weight, void *h_new, void *n, float alpha,
+                             float beta, float eps, unsigned flags, int64_t N, int D,
+                             la2_dtype dt, cudaStream_t stream);
+la2_status la2_residual_norm_backward(const void *dn, const void *dh_new, const void *h_new,
+                                      la2_dtype h_dt, const void *y, const float *weight,
+                                      const float *post_weight, void *dh, void *dy,
+                                      float *dweight, float *dpost_weight, float alpha,
+                                      float beta, float eps, unsigned flags, int64_t N, int D,
+                                      la2_dtype dt, void *workspace, size_t workspace_bytes,
+                                      cudaStream_t stream);
+
+/*
  * State pool for serving: the recurrent states of many requests live in one
  * fp32 array kv_pool [pool_size, H, d, e]; request b of a call uses state
  * slots[b] (device int32 [B], 4-byte aligned).  A negative slot marks an
@@ -356,6 +489,28 @@ la2_status la2_decode_tokens(const void *q, const void *k, const void *v,
                              const float *lambda, float *kv_pool, const int32_t *slots,
                              int pool_size, void *o, int B, int H, int T, int d, int e,
                              la2_dtype dt, cudaStream_t stream);
+
+/*
+ * States moved between slots: to[dst[n]] = from[src[n]] for n = 0..N-1, all
+ * at once (every source as it was before the call).  from fp32
+ * [layers, from_size, H, d, e] and to [layers, to_size, H, d, e] are one pool
+ * (the same pointer and size: any slot may be a source, a destination or
+ * both) or two that share no byte; the moves are the same in every layer.  A
+ * fork repeats a source; a beam reorder is a permutation with repeats; a
+ * compaction moves live slots down.  src, dst device int32 [N] (4-byte
+ * aligned): src[n] < 0 clears the destination (a new request's zero state),
+ * dst[n] < 0 is no move.  A slot past its pool is not checked on the host
+ * (that would synchronise): that move is skipped and the bounds bit of the
+ * device error word set.  The caller keeps the destinations of a call
+ * distinct (two moves to one slot leave bytes of either in it).
+ * No scratch memory: each CTA reads the same few bytes of every source before
+ * it writes any destination.  Errors: LA2_ERR_INVALID for negative sizes, NULL
+ * or misaligned pointers, pools that partly overlap or tables inside a pool;
+ * LA2_ERR_UNSUPPORTED for another d or e, or N above 4,096.
+ */
+la2_status la2_pool_copy(const float *from, int from_size, float *to, int to_size,
+                         const int32_t *src, const int32_t *dst, int N, int layers, int H, int d,
+                         int e, cudaStream_t stream);
 
 /*
  * Sequence sharding: a sequence of R * L rows cut into R shards of L rows
