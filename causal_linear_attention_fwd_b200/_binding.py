@@ -7,10 +7,12 @@ library is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import json
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -27,12 +29,6 @@ LA2_OPT_VARLEN_ORDER, LA2_OPT_DECODE_BLOCK_TOKENS, LA2_OPT_BWD_FORM = 5, 6, 7
 
 _lock = threading.Lock()
 _lib = None
-
-
-class _Heads(ctypes.Structure):
-    """la2_heads: a [B, heads, L, width] tensor by its first value and strides."""
-    _fields_ = [("p", ctypes.c_void_p), ("batch", ctypes.c_int64), ("head", ctypes.c_int64),
-                ("row", ctypes.c_int64)]
 
 
 class LA2Error(RuntimeError):
@@ -93,10 +89,10 @@ def library():
         lib.la2_feature_map.restype = I
         lib.la2_feature_map_backward.argtypes = [P, P, P, P, P, P, I64, I, P]
         lib.la2_feature_map_backward.restype = I
-        HP, F, U = ctypes.POINTER(_Heads), ctypes.c_float, ctypes.c_uint
-        lib.la2_rotary.argtypes = [HP, HP, HP, P, P, I, P, P, P, F, U, I, I, I, I64, I, I, I, I, P]
+        F, U = ctypes.c_float, ctypes.c_uint
+        lib.la2_rotary.argtypes = [P, P, P, P, P, I, P, P, P, F, U, I, I, I, I64, I, I, I, I, P]
         lib.la2_rotary.restype = I
-        lib.la2_rotary_backward.argtypes = [P, P, P, P, P, I, HP, HP, HP, F, U, I, I, I, I64, I, I,
+        lib.la2_rotary_backward.argtypes = [P, P, P, P, P, I, P, P, P, F, U, I, I, I, I64, I, I,
                                             I, I, P]
         lib.la2_rotary_backward.restype = I
         lib.la2_gated_norm.argtypes = [P, P, I64, I64, P, P, F, U, I, I, I64, I, I, P]
@@ -609,31 +605,65 @@ LA2_POSITIONS_ROW, LA2_POSITIONS_START, LA2_POSITIONS_TABLE = 0, 1, 2
 LA2_NORM_SILU, LA2_NORM_ROW, LA2_NORM_SHARED_WEIGHT, LA2_NORM_POST = 1, 2, 4, 8
 
 
-def _like(dev, **named):
-    """CUDA tensors (None skipped) on `dev`, any strides."""
-    for name, t in named.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+# The calls below are also made for single tokens, where the host's part of a
+# call is what it costs: their checks read each property of a tensor once, and
+# a device that is already current is not made current again.
+_no_guard = contextlib.nullcontext()
 
 
-def _strides(name, t, dims):
-    """The strides of a tensor's leading `dims` axes; its last axis is dense.
-    An axis of one entry has no stride that matters."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+def _cuda(name, t):
+    """The device of a call's first tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _on(dev, name, t, dense=True):
+    """A tensor (or None) on `dev`, contiguous unless not dense."""
+    if t is None:
+        return
+    if t.device != dev:
+        _cuda(name, t)
+        raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _guard(dev):
+    return _no_guard if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _raw_stream(stream, dev):
+    if stream is not None:
+        return _stream(stream, dev)
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _row_strides(name, t):
+    """A [B,L,columns] tensor's strides of batch and row."""
+    st = t.stride()
+    if st[2] != 1 and t.shape[2] > 1:
         raise ValueError(f"{name}'s last axis must be contiguous")
-    return [0 if t.shape[i] <= 1 else t.stride(i) for i in range(dims)]
+    return st[0], st[1]
+
+
+_pack_heads = struct.Struct("=qqqq").pack  # la2_heads
 
 
 def _heads(name, t):
-    return _Heads(t.data_ptr(), *_strides(name, t, 3))
-
-
-def _ref(x):
-    return None if x is None else ctypes.byref(x)
+    """la2_heads of a [B,heads,L,width] tensor: its first value and strides."""
+    st = t.stride()
+    if st[3] != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    return _pack_heads(t.data_ptr(), st[0], st[1], st[2])
 
 
 def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, factor: float = 1.0,
@@ -676,16 +706,17 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, factor: float 
 
 
 def _rotary_args(inv_freq, positions, B, L, dev):
+    """(columns that turn, the kind of positions)"""
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
         raise ValueError("inv_freq must be float64 [rotary_dim / 2]")
-    kind = LA2_POSITIONS_ROW
-    if positions is not None:
-        if positions.dtype != torch.int64 or tuple(positions.shape) not in ((B,), (B, L)):
-            raise ValueError("positions must be int64 [B] or [B,L]")
-        kind = LA2_POSITIONS_START if positions.dim() == 1 else LA2_POSITIONS_TABLE
-    if _devices(("inv_freq", inv_freq), ("positions", positions)) != dev:
-        raise ValueError(f"inv_freq is on {inv_freq.device}, other arguments on {dev}")
-    return kind
+    _on(dev, "inv_freq", inv_freq)
+    r = 2 * inv_freq.shape[0]
+    if positions is None:
+        return r, LA2_POSITIONS_ROW
+    if positions.dtype != torch.int64 or tuple(positions.shape) not in ((B,), (B, L)):
+        raise ValueError("positions must be int64 [B] or [B,L]")
+    _on(dev, "positions", positions)
+    return r, LA2_POSITIONS_START if positions.dim() == 1 else LA2_POSITIONS_TABLE
 
 
 def rotary(q, k, inv_freq, positions=None, *, v=None, interleaved: bool = False,
@@ -700,36 +731,40 @@ def rotary(q, k, inv_freq, positions=None, *, v=None, interleaved: bool = False,
     positions: None (row t is position t), int64 [B] (row t of request b is
     positions[b] + t) or int64 [B,L].  Returns (rq, rk), or with v (rq, rk, rv);
     out: buffers for them."""
-    lib = library()
-    if not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor")
-    dev = q.device
-    _like(dev, k=k, v=v)
-    B, H, L, d = q.shape
-    Hk, e = k.shape[1], (d if v is None else v.shape[-1])
-    if tuple(k.shape) != (B, Hk, L, d) or (v is not None and tuple(v.shape) != (B, Hk, L, e)):
+    lib = _lib or library()
+    dev = _cuda("q", q)
+    _on(dev, "k", k, False)
+    _on(dev, "v", v, False)
+    B, H, L, d = shape = q.shape
+    kshape, dtype = k.shape, q.dtype
+    Hk = kshape[1]
+    e = d if v is None else v.shape[-1]
+    if kshape != (B, Hk, L, d) or (v is not None and v.shape != (B, Hk, L, e)):
         raise ValueError("q must be [B,H,L,d], k [B,Hk,L,d] and v [B,Hk,L,e]")
     if H != Hk and (Hk == 0 or H % Hk):
         raise ValueError("H must be a multiple of Hk")
-    if k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+    if k.dtype != dtype or (v is not None and v.dtype != dtype):
         raise ValueError("q, k and v must have one dtype")
-    kind = _rotary_args(inv_freq, positions, B, L, dev)
-    with torch.cuda.device(dev):
-        shapes = ((B, H, L, d), (B, H, L, d), (B, H, L, e))[:2 if v is None else 3]
+    r, kind = _rotary_args(inv_freq, positions, B, L, dev)
+    with _guard(dev):
         if out is None:
-            outs = [torch.empty(s, dtype=q.dtype, device=dev) for s in shapes]
+            rq, rk = q.new_empty(shape), q.new_empty(shape)
+            rv = None if v is None else q.new_empty((B, H, L, e))
         else:
-            if len(out) != len(shapes):
-                raise ValueError(f"out must be {len(shapes)} buffers")
-            outs = [_out(t, f"out[{i}]", s, q.dtype, dev) for i, (t, s) in enumerate(zip(out, shapes))]
-        code = lib.la2_rotary(_ref(_heads("q", q)), _ref(_heads("k", k)),
-                              None if v is None else _ref(_heads("v", v)), _ptr(inv_freq),
-                              _ptr(positions), kind, _ptr(outs[0]), _ptr(outs[1]),
-                              None if v is None else _ptr(outs[2]), float(scale),
-                              LA2_ROTARY_INTERLEAVED if interleaved else 0, B, H, Hk, L, d, e,
-                              2 * inv_freq.numel(), _dt(q), _stream(stream, dev))
+            if len(out) != (2 if v is None else 3):
+                raise ValueError(f"out must be {2 if v is None else 3} buffers")
+            rq, rk, rv = (*out, None)[:3]
+            _out(rq, "out[0]", shape, dtype, dev)
+            _out(rk, "out[1]", shape, dtype, dev)
+            if v is not None:
+                _out(rv, "out[2]", (B, H, L, e), dtype, dev)
+        code = lib.la2_rotary(_heads("q", q), _heads("k", k), None if v is None else _heads("v", v),
+                              inv_freq.data_ptr(), _at(positions), kind, rq.data_ptr(),
+                              rk.data_ptr(), _at(rv), scale,
+                              LA2_ROTARY_INTERLEAVED if interleaved else 0, B, H, Hk, L, d, e, r,
+                              _dt(q), _raw_stream(stream, dev))
     _check(code, "la2_rotary")
-    return tuple(outs)
+    return (rq, rk) if v is None else (rq, rk, rv)
 
 
 def rotary_backward(dq, dk, inv_freq, positions=None, *, dv=None, kv_heads=None,
@@ -741,36 +776,39 @@ def rotary_backward(dq, dk, inv_freq, positions=None, *, dv=None, kv_heads=None,
     those shapes to write, strided views allowed (slices of a fused
     projection's gradient); by default views of token-major [B,L,heads,.]
     buffers."""
-    lib = library()
-    dev = _devices(("dq", dq), ("dk", dk), ("dv", dv))
-    B, H, L, d = dq.shape
+    lib = _lib or library()
+    dev = _cuda("dq", dq)
+    _on(dev, "dq", dq)
+    _on(dev, "dk", dk)
+    _on(dev, "dv", dv)
+    B, H, L, d = shape = dq.shape
+    dtype = dq.dtype
     Hk, e = H if kv_heads is None else int(kv_heads), (d if dv is None else dv.shape[-1])
-    if dk.shape != dq.shape or (dv is not None and tuple(dv.shape) != (B, H, L, e)):
+    if dk.shape != shape or (dv is not None and dv.shape != (B, H, L, e)):
         raise ValueError("dq, dk must be [B,H,L,d] and dv [B,H,L,e]")
     if Hk < 0 or (H != Hk and (Hk == 0 or H % Hk)):
         raise ValueError("H must be a multiple of kv_heads")
-    if dk.dtype != dq.dtype or (dv is not None and dv.dtype != dq.dtype):
+    if dk.dtype != dtype or (dv is not None and dv.dtype != dtype):
         raise ValueError("dq, dk and dv must have one dtype")
-    kind = _rotary_args(inv_freq, positions, B, L, dev)
-    with torch.cuda.device(dev):
+    r, kind = _rotary_args(inv_freq, positions, B, L, dev)
+    with _guard(dev):
         shapes = ((B, H, L, d), (B, Hk, L, d), (B, Hk, L, e))[:2 if dv is None else 3]
         if out is None:
-            outs = [torch.empty((b, n, h, w), dtype=dq.dtype, device=dev).transpose(1, 2)
-                    for b, h, n, w in shapes]
+            outs = [dq.new_empty((b, n, h, w)).transpose(1, 2) for b, h, n, w in shapes]
         else:
             if len(out) != len(shapes):
                 raise ValueError(f"out must be {len(shapes)} tensors")
             outs = list(out)
-            for i, (t, s) in enumerate(zip(outs, shapes)):
-                _like(dev, **{f"out[{i}]": t})
-                if tuple(t.shape) != s or t.dtype != dq.dtype:
-                    raise ValueError(f"out[{i}] must be {dq.dtype} {s}")
-        views = [_heads(f"out[{i}]", t) for i, t in enumerate(outs)]
-        code = lib.la2_rotary_backward(_ptr(dq), _ptr(dk), _ptr(dv), _ptr(inv_freq),
-                                       _ptr(positions), kind, _ref(views[0]), _ref(views[1]),
-                                       None if dv is None else _ref(views[2]), float(scale),
+            for i, (x, s) in enumerate(zip(outs, shapes)):
+                _on(dev, "out", x, False)
+                if x.shape != s or x.dtype != dtype:
+                    raise ValueError(f"out[{i}] must be {dtype} {s}")
+        views = [_heads("out", x) for x in outs]
+        code = lib.la2_rotary_backward(dq.data_ptr(), dk.data_ptr(), _at(dv), inv_freq.data_ptr(),
+                                       _at(positions), kind, views[0], views[1],
+                                       None if dv is None else views[2], scale,
                                        LA2_ROTARY_INTERLEAVED if interleaved else 0, B, H, Hk, L,
-                                       d, e, 2 * inv_freq.numel(), _dt(dq), _stream(stream, dev))
+                                       d, e, r, _dt(dq), _raw_stream(stream, dev))
     _check(code, "la2_rotary_backward")
     return tuple(outs)
 
@@ -780,15 +818,19 @@ def _gated_args(o, gate, weight, activation, per_head, dev):
     if activation not in ("silu", "sigmoid"):
         raise ValueError(f"unknown activation {activation!r}")
     flags = (LA2_NORM_SILU if activation == "silu" else 0) | (0 if per_head else LA2_NORM_ROW)
-    _like(dev, gate=gate)
-    if gate is not None and (tuple(gate.shape) != (B, L, H * e) or gate.dtype != o.dtype):
-        raise ValueError("gate must be [B,L,H*e] of o's dtype")
+    _on(dev, "o", o)
+    if gate is not None:
+        _on(dev, "gate", gate, False)
+        if gate.shape != (B, L, H * e) or gate.dtype != o.dtype:
+            raise ValueError("gate must be [B,L,H*e] of o's dtype")
     if weight is not None:
+        _on(dev, "weight", weight)
+        n = weight.numel()
         if weight.dtype != torch.float32 or weight.dim() != 1:
             raise ValueError("weight must be float32 [H*e] or [e]")
-        if per_head and weight.numel() == e:
+        if per_head and n == e:
             flags |= LA2_NORM_SHARED_WEIGHT
-        elif weight.numel() != H * e:
+        elif n != H * e:
             raise ValueError("weight must be float32 [H*e], or [e] for a norm per head")
     return B, H, L, e, flags
 
@@ -801,15 +843,15 @@ def gated_norm(o, gate=None, weight=None, *, activation: str = "silu", per_head:
     token's whole row.  gate [B,L,H*e] may be a view with strided batches and
     rows (a slice of a fused projection); a is "silu" or "sigmoid".  weight
     float32 [H*e], or [e] for all heads alike (per head only), or None."""
-    lib = library()
-    dev = _devices(("o", o), ("weight", weight))
+    lib = _lib or library()
+    dev = _cuda("o", o)
     B, H, L, e, flags = _gated_args(o, gate, weight, activation, per_head, dev)
-    with torch.cuda.device(dev):
+    with _guard(dev):
         u = (_out(out, "out", (B, L, H * e), o.dtype, dev) if out is not None
-             else torch.empty((B, L, H * e), dtype=o.dtype, device=dev))
-        sb, sl = (0, 0) if gate is None else _strides("gate", gate, 2)
-        code = lib.la2_gated_norm(_ptr(o), _ptr(gate), sb, sl, _ptr(weight), _ptr(u), float(eps),
-                                  flags, B, H, L, e, _dt(o), _stream(stream, dev))
+             else o.new_empty((B, L, H * e)))
+        sb, sl = (0, 0) if gate is None else _row_strides("gate", gate)
+        code = lib.la2_gated_norm(o.data_ptr(), _at(gate), sb, sl, _at(weight), u.data_ptr(), eps,
+                                  flags, B, H, L, e, _dt(o), _raw_stream(stream, dev))
     _check(code, "la2_gated_norm")
     return u
 
@@ -821,46 +863,52 @@ def gated_norm_backward(du, o, gate=None, weight=None, *, activation: str = "sil
     [B,L,H*e]; dgate is None without a gate, dweight (float32, of weight's
     shape) None without a weight.  out: (do, dgate) to write; dgate may be a
     view with strided batches and rows."""
-    lib = library()
-    dev = _devices(("du", du), ("o", o), ("weight", weight), ("workspace", workspace))
+    lib = _lib or library()
+    dev = _cuda("du", du)
+    _on(dev, "du", du)
+    _on(dev, "workspace", workspace)
     B, H, L, e, flags = _gated_args(o, gate, weight, activation, per_head, dev)
-    if tuple(du.shape) != (B, L, H * e) or du.dtype != o.dtype:
+    dtype = o.dtype
+    if du.shape != (B, L, H * e) or du.dtype != dtype:
         raise ValueError("du must be [B,L,H*e] of o's dtype")
-    with torch.cuda.device(dev):
+    with _guard(dev):
         if out is not None:
             do, dgate = out
-            _out(do, "do", o.shape, o.dtype, dev)
+            _out(do, "do", o.shape, dtype, dev)
             if (dgate is None) != (gate is None):
                 raise ValueError("gate and dgate are both given or both None")
-            _like(dev, dgate=dgate)
-            if dgate is not None and (dgate.shape != gate.shape or dgate.dtype != o.dtype):
-                raise ValueError("dgate must match gate's shape and dtype")
+            if dgate is not None:
+                _on(dev, "dgate", dgate, False)
+                if dgate.shape != gate.shape or dgate.dtype != dtype:
+                    raise ValueError("dgate must match gate's shape and dtype")
         else:
             do = torch.empty_like(o)
-            dgate = None if gate is None else torch.empty((B, L, H * e), dtype=o.dtype, device=dev)
+            dgate = None if gate is None else o.new_empty((B, L, H * e))
         dw = None if weight is None else torch.empty_like(weight)
         if workspace is None and dw is not None:
             workspace = _workspace(
-                workspace_size(LA2_OP_GATED_NORM_BACKWARD, B, H, L, e, e, o.dtype), dev)
-        sb, sl = (0, 0) if gate is None else _strides("gate", gate, 2)
-        tb, tl = (0, 0) if gate is None else _strides("dgate", dgate, 2)
-        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        code = lib.la2_gated_norm_backward(_ptr(du), _ptr(o), _ptr(gate), sb, sl, _ptr(weight),
-                                           _ptr(do), _ptr(dgate), tb, tl, _ptr(dw), float(eps),
-                                           flags, B, H, L, e, _dt(o), _ptr(workspace), nbytes,
-                                           _stream(stream, dev))
+                workspace_size(LA2_OP_GATED_NORM_BACKWARD, B, H, L, e, e, dtype), dev)
+        sb, sl = (0, 0) if gate is None else _row_strides("gate", gate)
+        tb, tl = (0, 0) if gate is None else _row_strides("dgate", dgate)
+        code = lib.la2_gated_norm_backward(du.data_ptr(), o.data_ptr(), _at(gate), sb, sl,
+                                           _at(weight), do.data_ptr(), _at(dgate), tb, tl, _at(dw),
+                                           eps, flags, B, H, L, e, _dt(o), _at(workspace),
+                                           _nbytes(workspace), _raw_stream(stream, dev))
     _check(code, "la2_gated_norm_backward")
     return do, dgate, dw
 
 
-def _residual_args(x, weight, post_weight, post_norm):
+def _residual_args(x, weight, post_weight, post_norm, dev):
+    """(rows, their width, flags)"""
     D = x.shape[-1]
     for name, w in (("weight", weight), ("post_weight", post_weight)):
-        if w is not None and (w.dtype != torch.float32 or tuple(w.shape) != (D,)):
-            raise ValueError(f"{name} must be float32 [D]")
+        if w is not None:
+            _on(dev, name, w)
+            if w.dtype != torch.float32 or w.shape != (D,):
+                raise ValueError(f"{name} must be float32 [D]")
     if post_weight is not None and not post_norm:
         raise ValueError("post_weight is given but post_norm is False")
-    return D, LA2_NORM_POST if post_norm else 0
+    return x.numel() // D if D else 0, D, LA2_NORM_POST if post_norm else 0
 
 
 def residual_norm(h, y=None, weight=None, *, post_norm: bool = False, post_weight=None,
@@ -873,24 +921,32 @@ def residual_norm(h, y=None, weight=None, *, post_norm: bool = False, post_weigh
     y's.  Returns (h_new, n); without y the norm of h alone, (h, n), n of
     `dtype` (h's when None).  out: (h_new, n) to write, which may be h and y
     themselves; without y, n."""
-    lib = library()
-    dev = _devices(("h", h), ("y", y), ("weight", weight), ("post_weight", post_weight))
-    D, flags = _residual_args(h, weight, post_weight, post_norm)
-    if y is None and (post_norm or alpha != 1.0):
-        raise ValueError("post_norm and alpha need a block output y")
-    if y is not None and (y.shape != h.shape or dtype not in (None, y.dtype)):
-        raise ValueError("y must match h's shape, and dtype y's")
-    dt = y.dtype if y is not None else (dtype or h.dtype)
-    with torch.cuda.device(dev):
-        h_new, n = (None, out) if y is None else (None, None) if out is None else out
-        if y is not None:
-            h_new = (_out(h_new, "h_new", h.shape, h.dtype, dev) if h_new is not None
-                     else torch.empty_like(h))
-        n = _out(n, "n", h.shape, dt, dev) if n is not None else torch.empty_like(h, dtype=dt)
-        code = lib.la2_residual_norm(_ptr(h), _dt(h), _ptr(y), _ptr(weight), _ptr(post_weight),
-                                     _ptr(h_new), _ptr(n), float(alpha), float(beta), float(eps),
-                                     flags, h.numel() // D if D else 0, D, _dt(n),
-                                     _stream(stream, dev))
+    lib = _lib or library()
+    dev = _cuda("h", h)
+    _on(dev, "h", h)
+    _on(dev, "y", y)
+    N, D, flags = _residual_args(h, weight, post_weight, post_norm, dev)
+    if y is None:
+        if post_norm or alpha != 1.0:
+            raise ValueError("post_norm and alpha need a block output y")
+        h_new, n, dt = None, out, dtype or h.dtype
+    else:
+        dt = y.dtype
+        if y.shape != h.shape or (dtype is not None and dtype != dt):
+            raise ValueError("y must match h's shape, and dtype y's")
+        h_new, n = (None, None) if out is None else out
+    with _guard(dev):
+        if h_new is not None:
+            _out(h_new, "h_new", h.shape, h.dtype, dev)
+        elif y is not None:
+            h_new = torch.empty_like(h)
+        if n is not None:
+            _out(n, "n", h.shape, dt, dev)
+        else:
+            n = torch.empty_like(h, dtype=dt) if y is None else torch.empty_like(y)
+        code = lib.la2_residual_norm(h.data_ptr(), _dt(h), _at(y), _at(weight), _at(post_weight),
+                                     _at(h_new), n.data_ptr(), alpha, beta, eps, flags, N, D,
+                                     _dt(n), _raw_stream(stream, dev))
     _check(code, "la2_residual_norm")
     return (h if y is None else h_new), n
 
@@ -904,36 +960,36 @@ def residual_norm_backward(dn, h_new, y=None, weight=None, *, dh_new=None, post_
     stored sum and y (needed with post_norm only) the block's output.  dweight
     and dpost_weight are None without their weights, dy with want_dy False (a
     call that had no y).  out: (dh, dy) to write; dh may be dh_new itself."""
-    lib = library()
-    dev = _devices(("dn", dn), ("h_new", h_new), ("y", y), ("weight", weight), ("dh_new", dh_new),
-                   ("post_weight", post_weight), ("workspace", workspace))
-    D, flags = _residual_args(h_new, weight, post_weight, post_norm)
+    lib = _lib or library()
+    dev = _cuda("dn", dn)
+    for name, x in (("dn", dn), ("h_new", h_new), ("y", y), ("dh_new", dh_new),
+                    ("workspace", workspace)):
+        _on(dev, name, x)
+    N, D, flags = _residual_args(h_new, weight, post_weight, post_norm, dev)
+    shape = h_new.shape
     if post_norm and y is None:
         raise ValueError("post_norm needs the block output y")
-    if dn.shape != h_new.shape or (y is not None and (y.shape != dn.shape or y.dtype != dn.dtype)):
+    if dn.shape != shape or (y is not None and (y.shape != shape or y.dtype != dn.dtype)):
         raise ValueError("dn and y must match h_new's shape and have one dtype")
-    if dh_new is not None and (dh_new.shape != h_new.shape or dh_new.dtype != h_new.dtype):
+    if dh_new is not None and (dh_new.shape != shape or dh_new.dtype != h_new.dtype):
         raise ValueError("dh_new must match h_new's shape and dtype")
-    with torch.cuda.device(dev):
+    with _guard(dev):
         dh, dy = (None, None) if out is None else out
-        dh = (_out(dh, "dh", h_new.shape, h_new.dtype, dev) if dh is not None
+        dh = (_out(dh, "dh", shape, h_new.dtype, dev) if dh is not None
               else torch.empty_like(h_new))
         if not want_dy:
             dy = None
         else:
-            dy = (_out(dy, "dy", dn.shape, dn.dtype, dev) if dy is not None
-                  else torch.empty_like(dn))
+            dy = _out(dy, "dy", shape, dn.dtype, dev) if dy is not None else torch.empty_like(dn)
         dw = None if weight is None else torch.empty_like(weight)
         dpw = None if post_weight is None else torch.empty_like(post_weight)
-        N = h_new.numel() // D if D else 0
         if workspace is None and (dw is not None or dpw is not None):
             workspace = _workspace(
                 workspace_size(LA2_OP_RESIDUAL_NORM_BACKWARD, 1, 1, N, D, D, dn.dtype), dev)
-        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         code = lib.la2_residual_norm_backward(
-            _ptr(dn), _ptr(dh_new), _ptr(h_new), _dt(h_new), _ptr(y), _ptr(weight),
-            _ptr(post_weight), _ptr(dh), _ptr(dy), _ptr(dw), _ptr(dpw), float(alpha), float(beta),
-            float(eps), flags, N, D, _dt(dn), _ptr(workspace), nbytes, _stream(stream, dev))
+            dn.data_ptr(), _at(dh_new), h_new.data_ptr(), _dt(h_new), _at(y), _at(weight),
+            _at(post_weight), dh.data_ptr(), _at(dy), _at(dw), _at(dpw), alpha, beta, eps, flags,
+            N, D, _dt(dn), _at(workspace), _nbytes(workspace), _raw_stream(stream, dev))
     _check(code, "la2_residual_norm_backward")
     return dh, dy, dw, dpw
 
@@ -945,23 +1001,27 @@ def pool_copy(pool, src, dst, *, source=None, stream=None):
     [P,H,d,e], or [layers,P,H,d,e] with the same moves in every layer; src, dst
     int32 [N], the destinations distinct.  source: another pool to copy from
     (same layers, H, d, e; any number of slots).  Returns pool."""
-    lib = library()
+    lib = _lib or library()
+    dev = _cuda("pool", pool)
     origin = pool if source is None else source
-    dev = _devices(("pool", pool), ("source", source), ("src", src), ("dst", dst))
-    for name, t in (("pool", pool), ("source", origin)):
-        if t.dtype != torch.float32 or t.dim() not in (4, 5):
-            raise ValueError(f"{name} must be float32 [P,H,d,e] or [layers,P,H,d,e]")
-    layers = pool.shape[0] if pool.dim() == 5 else 1
-    if (origin.dim() != pool.dim() or origin.shape[-3:] != pool.shape[-3:]
-            or (pool.dim() == 5 and origin.shape[0] != layers)):
+    for name, x in (("pool", pool), ("source", source), ("src", src), ("dst", dst)):
+        _on(dev, name, x)
+    shape, from_shape = pool.shape, origin.shape
+    dims = len(shape)
+    if dims not in (4, 5) or pool.dtype != torch.float32 or origin.dtype != torch.float32:
+        raise ValueError("pool and source must be float32 [P,H,d,e] or [layers,P,H,d,e]")
+    layers = shape[0] if dims == 5 else 1
+    H, d, e = shape[-3:]
+    if source is not None and (len(from_shape) != dims or from_shape[-3:] != (H, d, e)
+                               or (dims == 5 and from_shape[0] != layers)):
         raise ValueError("source must match pool but for its number of slots")
-    if src.dtype != torch.int32 or src.dim() != 1 or dst.dtype != torch.int32 or dst.shape != src.shape:
+    if (src.dtype != torch.int32 or src.dim() != 1 or dst.dtype != torch.int32
+            or dst.shape != src.shape):
         raise ValueError("src and dst must be int32 [N]")
-    H, d, e = pool.shape[-3:]
-    with torch.cuda.device(dev):
-        code = lib.la2_pool_copy(_ptr(origin), origin.shape[-4], _ptr(pool), pool.shape[-4],
-                                 _ptr(src), _ptr(dst), src.numel(), layers, H, d, e,
-                                 _stream(stream, dev))
+    with _guard(dev):
+        code = lib.la2_pool_copy(origin.data_ptr(), from_shape[-4], pool.data_ptr(), shape[-4],
+                                 src.data_ptr(), dst.data_ptr(), src.shape[0], layers, H, d, e,
+                                 _raw_stream(stream, dev))
     _check(code, "la2_pool_copy")
     return pool
 

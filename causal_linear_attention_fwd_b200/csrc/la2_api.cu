@@ -112,10 +112,13 @@ cudaError_t timed(int kid, cudaStream_t st, F &&launch) {
 
 // ------------------------------------------------------------- helpers
 int device_sms() {
+  static std::atomic<int> known[64];  // by device; 0: not asked yet
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 148;
+  if (dev < 64 && n > 0) known[dev].store(n, std::memory_order_relaxed);
   return n > 0 ? n : 148;
 }
 
@@ -607,13 +610,17 @@ bool all_aligned16(std::initializer_list<const void *> ps) {
 }
 bool dtype_ok(la2_dtype dt) { return dt == LA2_F32 || dt == LA2_BF16; }
 
-// CTAs per SM of a kernel, looked up once per kernel.
+// CTAs per SM of a kernel.  `last` keeps the answer for the last size of
+// shared memory asked about (size << 8 | CTAs).
 template <typename K>
-int resident(K kernel, int threads, size_t smem) {
+int resident(K kernel, int threads, size_t smem, std::atomic<uint64_t> &last) {
+  const uint64_t known = last.load(std::memory_order_relaxed);
+  if (known && known >> 8 == smem) return (int)(known & 255);
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess ||
       n < 1)
     n = 1;
+  last.store((uint64_t)smem << 8 | (uint64_t)n, std::memory_order_relaxed);
   return n;
 }
 
@@ -622,33 +629,50 @@ int resident(K kernel, int threads, size_t smem) {
 constexpr int kNormGradPerSm = 4;
 constexpr int kNormMaxCols = 16384;  // widest row that one CTA holds
 
-// How a gated norm's CTAs cover the columns: see gated_kernel.
-struct GatedPlan {
-  int nt, tpr, cols, slices, rpc;
+// How a norm's CTAs cover rows and columns.
+struct NormPlan {
+  int nt, tpr, nv, cols, slices, cl, rpc;
 };
-GatedPlan gated_plan(int H, int e, bool row) {
-  GatedPlan g;
-  const int D = H * e;
-  if (row) {
-    g.nt = D <= 512 ? 128 : D <= 4096 ? 256 : 512;
-    g.tpr = D <= 512 ? 32 : g.nt;
-    g.cols = D;
-    g.slices = 1;
+// The row's width decides who holds it (see la2_norm.cuh): a warp, a CTA with
+// one or two vectors per thread, or a cluster of CTAs.  `one` values at a time
+// where no 16-byte piece divides the row.
+NormPlan row_plan(int D, bool one) {
+  NormPlan g;
+  g.slices = 1;
+  const int most = one ? 2048 : 4096;
+  g.cl = 1;
+  while (g.cl * most < D) g.cl *= 2;
+  const int unit = one ? 1 : 8;
+  g.cols = ((D + unit - 1) / unit + g.cl - 1) / g.cl * unit;
+  if (!one && D <= 512) {
+    g.nt = 128;
+    g.tpr = 32;
+    g.nv = 2;
   } else {
-    // the most heads side by side that divide H, so no lane is idle
-    g.nt = 256;
-    int heads = g.nt * 8 / e;
-    while (H % heads) heads /= 2;
-    g.cols = heads * e;
-    g.tpr = g.cols / 8;
-    g.slices = H / heads;
+    g.nt = g.tpr = 256;
+    g.nv = one ? 8 : g.cols <= 2048 ? 1 : 2;
   }
   g.rpc = g.nt / g.tpr;
   return g;
 }
-int64_t grad_rows(int64_t rows, int rpc, int slices, int per_sm) {
-  const int64_t need = (rows + rpc - 1) / rpc;
-  const int64_t full = (int64_t)device_sms() * per_sm / slices;
+// Per head: the most heads side by side that divide H, so no lane is idle.
+NormPlan head_plan(int H, int e) {
+  NormPlan g;
+  g.nt = 256;
+  g.nv = 1;
+  g.cl = 1;
+  int heads = g.nt * 8 / e;
+  while (H % heads) heads /= 2;
+  g.cols = heads * e;
+  g.tpr = g.cols / 8;
+  g.slices = H / heads;
+  g.rpc = g.nt / g.tpr;
+  return g;
+}
+// Groups of CTAs (one row of partial sums each) that walk the rows.
+int64_t norm_groups(int64_t rows, const NormPlan &g, int per_sm) {
+  const int64_t need = (rows + g.rpc - 1) / g.rpc;
+  const int64_t full = (int64_t)device_sms() * per_sm / (g.slices * g.cl);
   return need < full ? need : (full > 1 ? full : 1);
 }
 
@@ -656,96 +680,141 @@ size_t norm_ws_bytes(int op, int B, int H, int64_t L, int d, int e, la2_dtype dt
   if (!dtype_ok(dt)) return 0;
   if (op == LA2_OP_RESIDUAL_NORM_BACKWARD) {
     if (d < 1 || d > kNormMaxCols) return 0;
-    const int64_t rows = (int64_t)B * H * L;
-    const int64_t most = (int64_t)device_sms() * kNormGradPerSm;
-    return (size_t)(rows < most ? rows : most) * d * sizeof(float) * 2;
+    return (size_t)norm_groups((int64_t)B * H * L, row_plan(d, d % 8 != 0), kNormGradPerSm) * d *
+           sizeof(float) * 2;
   }
   if (e != 64 && e != 128) return 0;
-  const int64_t rows = (int64_t)B * L;
-  int64_t most = 0;
-  for (int row = 0; row < 2; row++) {
-    if (row && (int64_t)H * e > kNormMaxCols) continue;
-    const GatedPlan g = gated_plan(H, e, row);
-    // a weight that the heads share has `slices` rows of e per CTA row, which
-    // is never more than one row of H * e
-    const int64_t n = grad_rows(rows, g.rpc, g.slices, kNormGradPerSm) * H * e;
+  const int64_t rows = (int64_t)B * L, D = (int64_t)H * e;
+  if (D > INT32_MAX) return 0;
+  // a weight that the heads share has `slices` rows of e per group, which is
+  // never more than one row of H * e
+  int64_t most = norm_groups(rows, head_plan(H, e), kNormGradPerSm);
+  if (D <= kNormMaxCols) {
+    const int64_t n = norm_groups(rows, row_plan((int)D, false), kNormGradPerSm);
     if (n > most) most = n;
   }
-  return (size_t)most * sizeof(float);
+  return (size_t)(most * D) * sizeof(float);
 }
 
 cudaError_t colsum(const float *a, const float *b, float *ya, float *yb, int64_t rows, int cols,
                    cudaStream_t st) {
   using namespace la2::norm;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)((cols + kSumCols - 1) / kSumCols), yb ? 2 : 1);
+  c.blockDim = dim3(kSumCols * kSumRows);
+  c.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
   return timed(K_NORM_WEIGHT_SUM, st, [&] {
-    colsum_kernel<<<dim3((unsigned)((cols + kSumCols - 1) / kSumCols), yb ? 2 : 1),
-                    kSumCols * kSumRows, 0, st>>>(a, b, ya, yb, (int)rows, cols);
+    return cudaLaunchKernelEx(&c, colsum_kernel, a, b, ya, yb, (int)rows, cols);
   });
 }
 
-template <typename T, bool ROW, bool GRAD, int NT, int NV>
-cudaError_t gated_launch(la2::norm::Gated p, const GatedPlan &g, float *dw, cudaStream_t st) {
-  auto kern = la2::norm::gated_kernel<T, ROW, GRAD, NT, NV>;
-  const size_t smem = GRAD && p.dw ? (size_t)NT * NV * 8 * sizeof(float) : 0;
-  if (cudaError_t e = opt_in_smem(kern, smem)) return e;
-  static const int per_sm = resident(kern, NT, (size_t)(GRAD ? NT * NV * 8 * sizeof(float) : 0));
-  const int cap = GRAD && per_sm > kNormGradPerSm ? kNormGradPerSm : per_sm;
-  const int64_t rows = grad_rows(p.rows, g.rpc, g.slices, cap);
-  cudaError_t e = timed(GRAD ? K_GATED_NORM_GRAD : K_GATED_NORM, st, [&] {
-    kern<<<dim3((unsigned)rows, (unsigned)g.slices), NT, smem, st>>>(p, g.tpr, g.cols);
-  });
+// A launch in clusters of g.cl CTAs along x.
+template <typename K, typename P>
+cudaError_t launch_groups(K kern, const P &p, const NormPlan &g, int64_t groups, size_t smem,
+                          cudaStream_t st) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)(groups * g.cl), (unsigned)g.slices);
+  c.blockDim = dim3((unsigned)g.nt);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim.x = (unsigned)g.cl;
+  a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+  c.attrs = a;
+  c.numAttrs = g.cl > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kern, p);
+}
+
+template <typename T, int E, bool ROW, bool GRAD, la2::norm::Gate GATE, int NT, int TPR, int NV>
+cudaError_t gated_launch(la2::norm::Gated p, const NormPlan &g, float *dw, cudaStream_t st) {
+  auto kern = la2::norm::gated_kernel<T, E, ROW, GRAD, GATE, NT, TPR, NV>;
+  constexpr size_t smem = GRAD ? (size_t)NT * NV * 8 * sizeof(float) : 0;
+  static std::atomic<uint64_t> last{0};
+  const int per_sm = resident(kern, NT, smem, last);
+  const int64_t groups =
+      norm_groups(p.rows, g, GRAD && per_sm > kNormGradPerSm ? kNormGradPerSm : per_sm);
+  p.cols = g.cols;
+  p.cl = g.cl;
+  p.tpr_shift = 0;
+  while (1 << p.tpr_shift < g.tpr) p.tpr_shift++;
+  cudaError_t e = timed(GRAD ? K_GATED_NORM_GRAD : K_GATED_NORM, st,
+                        [&] { return launch_groups(kern, p, g, groups, smem, st); });
   if (e != cudaSuccess || !GRAD || !dw) return e;
-  return p.shared ? colsum(p.dw, nullptr, dw, nullptr, rows * g.slices, p.e, st)
-                  : colsum(p.dw, nullptr, dw, nullptr, rows, p.H * p.e, st);
+  return p.shared ? colsum(p.dw, nullptr, dw, nullptr, groups * g.slices, p.e, st)
+                  : colsum(p.dw, nullptr, dw, nullptr, groups, p.H * p.e, st);
 }
 
+template <typename T, bool GRAD, la2::norm::Gate GATE>
+cudaError_t gated_shape(const la2::norm::Gated &p, bool row, float *dw, cudaStream_t st) {
+  if (!row) {
+    const NormPlan g = head_plan(p.H, p.e);
+    return p.e == 64 ? gated_launch<T, 64, false, GRAD, GATE, 256, 32, 1>(p, g, dw, st)
+                     : gated_launch<T, 128, false, GRAD, GATE, 256, 32, 1>(p, g, dw, st);
+  }
+  const NormPlan g = row_plan(p.H * p.e, false);
+  if (g.tpr == 32) return gated_launch<T, 0, true, GRAD, GATE, 128, 32, 2>(p, g, dw, st);
+  if (g.nv == 1) return gated_launch<T, 0, true, GRAD, GATE, 256, 256, 1>(p, g, dw, st);
+  return gated_launch<T, 0, true, GRAD, GATE, 256, 256, 2>(p, g, dw, st);
+}
 template <typename T, bool GRAD>
-cudaError_t gated_call(const la2::norm::Gated &p, bool row, float *dw, cudaStream_t st) {
-  const GatedPlan g = gated_plan(p.H, p.e, row);
-  if (!row) return gated_launch<T, false, GRAD, 256, 1>(p, g, dw, st);
-  if (g.nt == 128) return gated_launch<T, true, GRAD, 128, 2>(p, g, dw, st);
-  if (g.nt == 256) return gated_launch<T, true, GRAD, 256, 2>(p, g, dw, st);
-  return gated_launch<T, true, GRAD, 512, 4>(p, g, dw, st);
+cudaError_t gated_gate(const la2::norm::Gated &p, unsigned flags, float *dw, cudaStream_t st) {
+  using namespace la2::norm;
+  const bool row = (flags & LA2_NORM_ROW) != 0;
+  if (!p.gate) return gated_shape<T, GRAD, GATE_NONE>(p, row, dw, st);
+  return flags & LA2_NORM_SILU ? gated_shape<T, GRAD, GATE_SILU>(p, row, dw, st)
+                               : gated_shape<T, GRAD, GATE_SIGMOID>(p, row, dw, st);
+}
+template <bool GRAD>
+cudaError_t gated_call(const la2::norm::Gated &p, la2_dtype dt, unsigned flags, float *dw,
+                       cudaStream_t st) {
+  return dt == LA2_F32 ? gated_gate<float, GRAD>(p, flags, dw, st)
+                       : gated_gate<__nv_bfloat16, GRAD>(p, flags, dw, st);
 }
 
 template <typename T, typename R, bool POST, bool GRAD, int V, int NT, int TPR, int NV>
-cudaError_t residual_launch(la2::norm::Residual p, float *dw, float *dpw, cudaStream_t st) {
-  constexpr int RPC = NT / TPR;
-  const int sms = device_sms();
-  const int64_t need = (p.rows + RPC - 1) / RPC;
-  if constexpr (!GRAD) {
-    auto kern = la2::norm::residual_kernel<T, R, POST, V, NT, TPR, NV>;
-    static const int per_sm = resident(kern, NT, 0);
-    const int64_t full = (int64_t)sms * per_sm;
-    return timed(K_RESIDUAL_NORM, st, [&] {
-      kern<<<(unsigned)(need < full ? need : full), NT, 0, st>>>(p);
-    });
-  } else {
-    auto kern = la2::norm::residual_grad_kernel<T, R, POST, V, NT, TPR, NV>;
-    constexpr size_t smem = (size_t)NT * NV * V * sizeof(float) * (POST ? 2 : 1);
-    if (cudaError_t e = opt_in_smem(kern, smem)) return e;
-    static const int per_sm = resident(kern, NT, smem);
-    const int64_t full = (int64_t)sms * (per_sm < kNormGradPerSm ? per_sm : kNormGradPerSm);
-    const int64_t rows = need < full ? need : full;
-    if (dpw) p.dpw = p.dw + rows * p.D;
-    if (!dw) p.dw = nullptr;
-    cudaError_t e = timed(K_RESIDUAL_NORM_GRAD, st, [&] { kern<<<(unsigned)rows, NT, smem, st>>>(p); });
-    if (e != cudaSuccess || (!dw && !dpw)) return e;
-    return colsum(p.dw, p.dpw, dw, dpw, rows, p.D, st);
+cudaError_t residual_launch(la2::norm::Residual p, const NormPlan &g, float *dw, float *dpw,
+                            cudaStream_t st) {
+  auto kern = la2::norm::residual_kernel<T, R, GRAD, POST, V, NT, TPR, NV>;
+  size_t smem = 0;
+  if (V == 8 && TPR > 32) {
+    // two rows of every stream
+    size_t row = (size_t)g.cols * sizeof(R);
+    if (GRAD) row += (p.dh_new ? (size_t)g.cols * sizeof(R) : 0) + (size_t)g.cols * sizeof(T);
+    if (GRAD ? POST : p.y != nullptr) row += (size_t)g.cols * sizeof(T);
+    smem = la2::norm::kRingHead + 2 * ((row + 127) / 128 * 128);
+  } else if (GRAD && TPR == 32) {
+    smem = (size_t)NT * NV * V * sizeof(float);
   }
+  if (smem > 48 * 1024)
+    if (cudaError_t e = opt_in_smem(kern, smem)) return e;
+  static std::atomic<uint64_t> last{0};
+  int per_sm = resident(kern, NT, smem, last);
+  if (GRAD && per_sm > kNormGradPerSm) per_sm = kNormGradPerSm;
+  const int64_t groups = norm_groups(p.rows, g, per_sm);
+  p.cols = g.cols;
+  p.cl = g.cl;
+  if (GRAD && dpw) p.dpw = p.dw + groups * p.D;
+  if (!dw) p.dw = nullptr;
+  cudaError_t e = timed(GRAD ? K_RESIDUAL_NORM_GRAD : K_RESIDUAL_NORM, st,
+                        [&] { return launch_groups(kern, p, g, groups, smem, st); });
+  if (e != cudaSuccess || !GRAD || (!dw && !dpw)) return e;
+  return colsum(p.dw, p.dpw, dw, dpw, groups, p.D, st);
 }
 
-// Rows of whole 16-byte pieces (D a multiple of 8) move as vectors: a warp
-// per row up to 512 columns, else a CTA per row; other widths value by value.
 template <typename T, typename R, bool POST, bool GRAD>
 cudaError_t residual_shape(const la2::norm::Residual &p, float *dw, float *dpw, cudaStream_t st) {
-  if (p.D % 8 == 0) {
-    if (p.D <= 512) return residual_launch<T, R, POST, GRAD, 8, 128, 32, 2>(p, dw, dpw, st);
-    if (p.D <= 4096) return residual_launch<T, R, POST, GRAD, 8, 256, 256, 2>(p, dw, dpw, st);
-    return residual_launch<T, R, POST, GRAD, 8, 512, 512, 4>(p, dw, dpw, st);
-  }
-  if (p.D <= 2048) return residual_launch<T, R, POST, GRAD, 1, 256, 256, 8>(p, dw, dpw, st);
-  return residual_launch<T, R, POST, GRAD, 1, 1024, 1024, 16>(p, dw, dpw, st);
+  const bool one = p.D % 8 != 0;
+  const NormPlan g = row_plan(p.D, one);
+  if (one) return residual_launch<T, R, POST, GRAD, 1, 256, 256, 8>(p, g, dw, dpw, st);
+  if (g.tpr == 32) return residual_launch<T, R, POST, GRAD, 8, 128, 32, 2>(p, g, dw, dpw, st);
+  if (g.nv == 1) return residual_launch<T, R, POST, GRAD, 8, 256, 256, 1>(p, g, dw, dpw, st);
+  return residual_launch<T, R, POST, GRAD, 8, 256, 256, 2>(p, g, dw, dpw, st);
 }
 
 template <bool GRAD>
@@ -816,6 +885,13 @@ bool apart(const la2_heads &x, int nx, int wx, const la2_heads &y, int ny, int w
   return side_by_side(wx, wy, {{x.batch, B}, {x.row, L}, {nx > 1 ? x.head : y.head, n}});
 }
 
+template <typename T, bool GRAD, bool INTER>
+void rotary_launch(const la2::rot::Args &a, dim3 grid, size_t smem, bool vec, cudaStream_t st) {
+  using namespace la2::rot;
+  if (vec) rotary_kernel<T, GRAD, INTER, 8, sizeof(T) == 2 ? 4 : 2><<<grid, NT, smem, st>>>(a);
+  else rotary_kernel<T, GRAD, INTER, 1, 4><<<grid, NT, smem, st>>>(a);
+}
+
 template <bool GRAD>
 la2_status rotary_call(const la2_heads *q, const la2_heads *k, const la2_heads *v,
                        const double *inv_freq, const int64_t *positions, int kind, void *mq,
@@ -874,7 +950,6 @@ la2_status rotary_call(const la2_heads *q, const la2_heads *k, const la2_heads *
   a.rows = (int64_t)B * L;
   a.rep = H / Hk;
   a.r = r;
-  a.inter = (flags & LA2_ROTARY_INTERLEAVED) != 0;
   a.scale = scale;
   using namespace la2::rot;
   const int64_t tiles = (a.rows + TOK - 1) / TOK;
@@ -884,14 +959,14 @@ la2_status rotary_call(const la2_heads *q, const la2_heads *k, const la2_heads *
   const int64_t groups = (H + per - 1) / per, want = (4 * (int64_t)device_sms() + tiles - 1) / tiles;
   const dim3 grid((unsigned)tiles, (unsigned)(want < groups ? want : groups));
   const size_t smem = (size_t)TOK * (r / 2) * sizeof(float2);
+  const bool inter = (flags & LA2_ROTARY_INTERLEAVED) != 0;
   return to_status(timed(GRAD ? K_ROTARY_GRAD : K_ROTARY, stream, [&] {
-    if (dt == LA2_F32) {
-      if (vec) rotary_kernel<float, GRAD, 8><<<grid, NT, smem, stream>>>(a);
-      else rotary_kernel<float, GRAD, 1><<<grid, NT, smem, stream>>>(a);
-    } else {
-      if (vec) rotary_kernel<__nv_bfloat16, GRAD, 8><<<grid, NT, smem, stream>>>(a);
-      else rotary_kernel<__nv_bfloat16, GRAD, 1><<<grid, NT, smem, stream>>>(a);
-    }
+    if (dt == LA2_F32)
+      inter ? rotary_launch<float, GRAD, true>(a, grid, smem, vec, stream)
+            : rotary_launch<float, GRAD, false>(a, grid, smem, vec, stream);
+    else
+      inter ? rotary_launch<__nv_bfloat16, GRAD, true>(a, grid, smem, vec, stream)
+            : rotary_launch<__nv_bfloat16, GRAD, false>(a, grid, smem, vec, stream);
   }));
 }
 
@@ -905,7 +980,7 @@ la2_status gated_checks(unsigned flags, int B, int H, int64_t L, int e, float ep
   if ((flags & LA2_NORM_ROW) && (flags & LA2_NORM_SHARED_WEIGHT)) return LA2_ERR_INVALID;
   if (!dtype_ok(dt) || (e != 64 && e != 128)) return LA2_ERR_UNSUPPORTED;
   if ((flags & LA2_NORM_ROW) && (int64_t)H * e > kNormMaxCols) return LA2_ERR_UNSUPPORTED;
-  if ((int64_t)H * e > INT32_MAX) return LA2_ERR_UNSUPPORTED;
+  if ((int64_t)H * e > INT32_MAX || (H > 0 && head_plan(H, e).slices > 65535)) return LA2_ERR_UNSUPPORTED;
   if (reinterpret_cast<uintptr_t>(gate) % esize(dt)) return LA2_ERR_INVALID;
   *empty = (int64_t)B * H * L == 0;
   return LA2_OK;
@@ -1603,13 +1678,10 @@ la2_status la2_gated_norm(const void *o, const void *gate, int64_t gate_batch, i
   p.rows = (int64_t)B * L;
   p.H = H;
   p.e = e;
-  p.silu = (flags & LA2_NORM_SILU) != 0;
   p.shared = (flags & LA2_NORM_SHARED_WEIGHT) != 0;
   p.gate_vec = rows_vec(gate, gate_batch, gate_row, B, L, es);
   p.eps = eps;
-  const bool row = (flags & LA2_NORM_ROW) != 0;
-  return to_status(dt == LA2_F32 ? gated_call<float, false>(p, row, nullptr, stream)
-                                 : gated_call<__nv_bfloat16, false>(p, row, nullptr, stream));
+  return to_status(gated_call<false>(p, dt, flags, nullptr, stream));
 }
 
 la2_status la2_gated_norm_backward(const void *du, const void *o, const void *gate,
@@ -1655,14 +1727,11 @@ la2_status la2_gated_norm_backward(const void *du, const void *o, const void *ga
   p.rows = (int64_t)B * L;
   p.H = H;
   p.e = e;
-  p.silu = (flags & LA2_NORM_SILU) != 0;
   p.shared = (flags & LA2_NORM_SHARED_WEIGHT) != 0;
   p.gate_vec = rows_vec(gate, gate_batch, gate_row, B, L, es);
   p.dgate_vec = rows_vec(dgate, dgate_batch, dgate_row, B, L, es);
   p.eps = eps;
-  const bool row = (flags & LA2_NORM_ROW) != 0;
-  return to_status(dt == LA2_F32 ? gated_call<float, true>(p, row, dweight, stream)
-                                 : gated_call<__nv_bfloat16, true>(p, row, dweight, stream));
+  return to_status(gated_call<true>(p, dt, flags, dweight, stream));
 }
 
 la2_status la2_residual_norm(const void *h, la2_dtype h_dt, const void *y, const float *weight,

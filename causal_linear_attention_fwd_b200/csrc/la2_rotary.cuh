@@ -44,105 +44,152 @@ struct Args {
   const int64_t *pos;
   int pos_mode;        // 0: the row index; 1: pos[b] + row; 2: pos[b][row]
   int64_t L, rows;     // rows = B * L
-  int rep, r, inter;
+  int rep, r;
   float scale;
 };
 
 // V = 8: a lane moves 2 x 8 columns of one head (both members of 8 pairs);
 // V = 1: 2 columns, for widths, alignments or strides that 16-byte pieces do
-// not fit.
-template <typename T, bool GRAD, int V>
-__global__ void __launch_bounds__(NT) rotary_kernel(const __grid_constant__ Args a) {
+// not fit.  U heads' loads are issued before any of them is turned, and the
+// first ones before the table is made.
+template <typename T, bool GRAD, bool INTER, int V, int U>
+__global__ void __launch_bounds__(NT, 3) rotary_kernel(const __grid_constant__ Args a) {
   extern __shared__ float2 table[];  // [TOK][r / 2]
   const int64_t row0 = (int64_t)blockIdx.x * TOK;
   const int half = a.r / 2;
-  for (int i = threadIdx.x; i < TOK * half; i += NT) {
-    const int64_t row = row0 + i / half;
-    if (row >= a.rows) break;
-    const int64_t b = row / a.L, t = row - b * a.L;
-    const int64_t pos = a.pos_mode == 0 ? t : a.pos_mode == 1 ? a.pos[b] + t : a.pos[row];
-    // the angle less its whole turns, in fp64; what is left fits fp32
-    const double turns = (double)pos * a.freq[i % half] * 0.15915494309189533577;
-    float sn, cs;
-    sincospif(2.f * (float)(turns - rint(turns)), &sn, &cs);
-    table[i] = make_float2(cs * a.scale, (GRAD ? -sn : sn) * a.scale);
-  }
-  __syncthreads();
   const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES;
   const int64_t row = row0 + sub;
-  if (row >= a.rows) return;
-  const int64_t b = row / a.L, t = row - b * a.L;
-  const float2 *cs = table + sub * half;
-#pragma unroll
-  for (int q = 0; q < 3; q++) {
-    if (q >= a.parts) break;
+  const bool live = row < a.rows;
+  int64_t b = 0, t = 0;
+  if (live) norm::split_row(row, a.L, b, t);
+#pragma unroll 1
+  for (int q = 0; q < a.parts; q++) {
     const Part &p = a.part[q];
     const int rep = q == 0 ? 1 : a.rep;
     const int chunks = p.width / (2 * V);      // lanes of one head
     const int per = LANES / chunks;            // heads at a time
-    if (lane >= per * chunks) continue;
     const int c = lane % chunks;
     // the lane's columns: x0 from c0, x1 from c1
     const bool turned = c * 2 * V < p.turn;
-    const int c0 = turned && !a.inter ? c * V : c * 2 * V;
-    const int c1 = turned && !a.inter ? c0 + half : c0 + V;
+    const int c0 = turned && !INTER ? c * V : c * 2 * V;
+    const int c1 = turned && !INTER ? c0 + half : c0 + V;
+    const int64_t hstep = a.L * p.width;
     T *strided = static_cast<T *>(p.strided) + b * p.sb + t * p.sl;
     T *major = static_cast<T *>(p.major) + (b * p.n * rep * a.L + t) * p.width;
-    const int64_t hstep = a.L * p.width;
-    for (int h = blockIdx.y * per + lane / chunks; h < p.n; h += gridDim.y * per) {
-      float x0[V], x1[V];
-      T *s = strided + h * p.sh;
-      T *m = major + (int64_t)h * rep * hstep;
-      if constexpr (!GRAD) {
-        norm::ldv<T, V>(s + c0, x0);
-        norm::ldv<T, V>(s + c1, x1);
-      } else {
-        norm::ldv<T, V>(m + c0, x0);
-        norm::ldv<T, V>(m + c1, x1);
-        for (int j = 1; j < rep; j++) {
-          float y0[V], y1[V];
-          norm::ldv<T, V>(m + j * hstep + c0, y0);
-          norm::ldv<T, V>(m + j * hstep + c1, y1);
+    const int h0 = blockIdx.y * per + lane / chunks, stride = gridDim.y * per;
+    const int n = live ? p.n : 0;
+    norm::Raw<T, V> x0[U], x1[U];
+    auto fetch = [&](int h) {
 #pragma unroll
-          for (int i = 0; i < V; i++) {
-            x0[i] += y0[i];
-            x1[i] += y1[i];
+      for (int u = 0; u < U; u++) {
+        const int hu = h + u * stride;
+        if (hu < n) {
+          const T *s = GRAD ? major + (int64_t)hu * hstep : strided + hu * p.sh;
+          x0[u].load(s + c0);
+          x1[u].load(s + c1);
+        }
+      }
+    };
+    const bool sums = GRAD && rep > 1;  // a head's gradients come from several
+    if (!sums) fetch(h0);
+    if (q == 0) {
+#pragma unroll 1
+      for (int i = threadIdx.x; i < TOK * half; i += NT) {
+        const int64_t r = row0 + i / half;
+        if (r >= a.rows) break;
+        int64_t rb, rt;
+        norm::split_row(r, a.L, rb, rt);
+        const int64_t pos = a.pos_mode == 0 ? rt : a.pos_mode == 1 ? a.pos[rb] + rt : a.pos[r];
+        // the angle less its whole turns, in fp64; what is left fits fp32
+        const double turns = (double)pos * a.freq[i % half] * 0.15915494309189533577;
+        float sn, cs;
+        sincospif(2.f * (float)(turns - rint(turns)), &sn, &cs);
+        table[i] = make_float2(cs * a.scale, (GRAD ? -sn : sn) * a.scale);
+      }
+      __syncthreads();
+    }
+    float2 w[V];
+    if (turned && live) {
+#pragma unroll
+      for (int i = 0; i < V; i++) w[i] = table[sub * half + c * V + i];
+    }
+    auto turn = [&](float (&f)[V], float (&g)[V]) {
+      if (!turned) return;
+      if (V > 1 && INTER) {
+        // pairs are neighbours: f holds the first V / 2 pairs, g the rest
+#pragma unroll
+        for (int i = 0; i + 1 < V; i += 2) {
+          const float2 u = w[i / 2], v = w[V / 2 + i / 2];
+          const float f0 = f[i], g0 = g[i];
+          f[i] = f0 * u.x - f[i + 1] * u.y;
+          f[i + 1] = f0 * u.y + f[i + 1] * u.x;
+          g[i] = g0 * v.x - g[i + 1] * v.y;
+          g[i + 1] = g0 * v.y + g[i + 1] * v.x;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+          const float f0 = f[i];
+          f[i] = f0 * w[i].x - g[i] * w[i].y;
+          g[i] = f0 * w[i].y + g[i] * w[i].x;
+        }
+      }
+    };
+    if (!sums) {
+      for (int h = h0; h < n; h += U * stride) {
+        if (h != h0) fetch(h);
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+          const int hu = h + u * stride;
+          if (hu >= n) break;
+          float f[V], g[V];
+          x0[u].get(f);
+          x1[u].get(g);
+          turn(f, g);
+          if constexpr (GRAD) {
+            norm::stv<T, V>(strided + hu * p.sh + c0, f);
+            norm::stv<T, V>(strided + hu * p.sh + c1, g);
+          } else {
+            T *m = major + (int64_t)hu * rep * hstep;
+#pragma unroll 1
+            for (int j = 0; j < rep; j++, m += hstep) {
+              norm::stv<T, V>(m + c0, f);
+              norm::stv<T, V>(m + c1, g);
+            }
           }
         }
       }
-      if (turned) {
-        const float2 *w = cs + c * V;
-        if (V > 1 && a.inter) {
-          // pairs are neighbours: x0 holds the first V / 2 pairs, x1 the rest
+    } else {
+      for (int h = h0; h < n; h += stride) {
+        const T *m = major + (int64_t)h * rep * hstep;
+        float f[V], g[V];
 #pragma unroll
-          for (int i = 0; i < V; i += 2) {
-            const float2 u = w[i / 2], v = w[V / 2 + i / 2];
-            float f = x0[i], g = x0[i + (V > 1)];
-            x0[i] = f * u.x - g * u.y;
-            x0[i + (V > 1)] = f * u.y + g * u.x;
-            f = x1[i];
-            g = x1[i + (V > 1)];
-            x1[i] = f * v.x - g * v.y;
-            x1[i + (V > 1)] = f * v.y + g * v.x;
+        for (int i = 0; i < V; i++) f[i] = g[i] = 0.f;
+        for (int j = 0; j < rep; j += U) {
+#pragma unroll
+          for (int u = 0; u < U; u++) {
+            if (j + u < rep) {
+              x0[u].load(m + (j + u) * hstep + c0);
+              x1[u].load(m + (j + u) * hstep + c1);
+            }
           }
-        } else {
 #pragma unroll
-          for (int i = 0; i < V; i++) {
-            const float2 u = w[i];
-            const float f = x0[i], g = x1[i];
-            x0[i] = f * u.x - g * u.y;
-            x1[i] = f * u.y + g * u.x;
+          for (int u = 0; u < U; u++) {
+            if (j + u < rep) {
+              float y0[V], y1[V];
+              x0[u].get(y0);
+              x1[u].get(y1);
+#pragma unroll
+              for (int i = 0; i < V; i++) {
+                f[i] += y0[i];
+                g[i] += y1[i];
+              }
+            }
           }
         }
-      }
-      if constexpr (!GRAD) {
-        for (int j = 0; j < rep; j++) {
-          norm::stv<T, V>(m + j * hstep + c0, x0);
-          norm::stv<T, V>(m + j * hstep + c1, x1);
-        }
-      } else {
-        norm::stv<T, V>(s + c0, x0);
-        norm::stv<T, V>(s + c1, x1);
+        turn(f, g);
+        norm::stv<T, V>(strided + h * p.sh + c0, f);
+        norm::stv<T, V>(strided + h * p.sh + c1, g);
       }
     }
   }

@@ -25,8 +25,13 @@ def lib():
     return la2.library()
 
 
+class Heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("batch", ctypes.c_int64), ("head", ctypes.c_int64),
+                ("row", ctypes.c_int64)]
+
+
 def heads(p, batch, head, row):
-    return None if p is None else ctypes.byref(B._Heads(p, batch, head, row))
+    return None if p is None else ctypes.byref(Heads(p, batch, head, row))
 
 
 def rotary(lib, q=Q, k=K, v=V, f=F, pos=None, kind=0, rq=RQ, rk=RK, rv=RV, flags=0, Bn=2, Hn=4, Hk=2,
