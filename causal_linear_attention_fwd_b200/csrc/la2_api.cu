@@ -650,7 +650,7 @@ NormPlan row_plan(int D, bool one) {
     g.nv = 2;
   } else {
     g.nt = g.tpr = 256;
-    g.nv = one ? 8 : g.cols <= 2048 ? 1 : 2;
+    g.nv = one || g.cols <= 2048 ? 1 : 2;
   }
   g.rpc = g.nt / g.tpr;
   return g;
@@ -777,19 +777,23 @@ cudaError_t gated_call(const la2::norm::Gated &p, la2_dtype dt, unsigned flags, 
                        : gated_gate<__nv_bfloat16, GRAD>(p, flags, dw, st);
 }
 
-template <typename T, typename R, bool POST, bool GRAD, int V, int NT, int TPR, int NV>
+template <typename T, typename R, bool POST, bool GRAD, bool ONE, int NT, int TPR, int NV>
 cudaError_t residual_launch(la2::norm::Residual p, const NormPlan &g, float *dw, float *dpw,
                             cudaStream_t st) {
-  auto kern = la2::norm::residual_kernel<T, R, GRAD, POST, V, NT, TPR, NV>;
+  auto kern = la2::norm::residual_kernel<T, R, GRAD, POST, ONE, NT, TPR, NV>;
   size_t smem = 0;
-  if (V == 8 && TPR > 32) {
-    // two rows of every stream
+  if (!ONE && TPR > 32) {
+    // the weights, and two rows of every stream where two CTAs on an SM have
+    // room for them, else one
     size_t row = (size_t)g.cols * sizeof(R);
     if (GRAD) row += (p.dh_new ? (size_t)g.cols * sizeof(R) : 0) + (size_t)g.cols * sizeof(T);
     if (GRAD ? POST : p.y != nullptr) row += (size_t)g.cols * sizeof(T);
-    smem = la2::norm::kRingHead + 2 * ((row + 127) / 128 * 128);
+    row = (row + 127) / 128 * 128;
+    const size_t head = la2::norm::kRingHead + (size_t)g.cols * sizeof(float) * (POST ? 2 : 1);
+    p.stages = head + 2 * row <= 112 * 1024 ? 2 : 1;
+    smem = head + p.stages * row;
   } else if (GRAD && TPR == 32) {
-    smem = (size_t)NT * NV * V * sizeof(float);
+    smem = (size_t)NT * NV * 8 * sizeof(float);
   }
   if (smem > 48 * 1024)
     if (cudaError_t e = opt_in_smem(kern, smem)) return e;
@@ -811,10 +815,10 @@ template <typename T, typename R, bool POST, bool GRAD>
 cudaError_t residual_shape(const la2::norm::Residual &p, float *dw, float *dpw, cudaStream_t st) {
   const bool one = p.D % 8 != 0;
   const NormPlan g = row_plan(p.D, one);
-  if (one) return residual_launch<T, R, POST, GRAD, 1, 256, 256, 8>(p, g, dw, dpw, st);
-  if (g.tpr == 32) return residual_launch<T, R, POST, GRAD, 8, 128, 32, 2>(p, g, dw, dpw, st);
-  if (g.nv == 1) return residual_launch<T, R, POST, GRAD, 8, 256, 256, 1>(p, g, dw, dpw, st);
-  return residual_launch<T, R, POST, GRAD, 8, 256, 256, 2>(p, g, dw, dpw, st);
+  if (one) return residual_launch<T, R, POST, GRAD, true, 256, 256, 1>(p, g, dw, dpw, st);
+  if (g.tpr == 32) return residual_launch<T, R, POST, GRAD, false, 128, 32, 2>(p, g, dw, dpw, st);
+  if (g.nv == 1) return residual_launch<T, R, POST, GRAD, false, 256, 256, 1>(p, g, dw, dpw, st);
+  return residual_launch<T, R, POST, GRAD, false, 256, 256, 2>(p, g, dw, dpw, st);
 }
 
 template <bool GRAD>

@@ -40,6 +40,8 @@
 // fixed order: no atomics, the same result on every run.
 #pragma once
 
+#include <type_traits>
+
 #include "la2_common.cuh"
 #include "la2_fmap.cuh"
 #include "la2_sm100.cuh"
@@ -49,11 +51,13 @@ namespace norm {
 
 using namespace sm100;
 
-// ------------------------------------------------------------ vectors
-// V values of T as they are in memory; V = 8 moves 16-byte pieces, V = 1
-// single values (rows that no vector divides).
-template <typename T, int V> struct Raw;
-template <typename T> struct Raw<T, 8> {
+// ------------------------------------------------------------ eight values
+// What a thread holds of a row: units of eight values as four pairs, so that
+// most arithmetic is done two at a time (mul2, fma2).  They are eight
+// neighbours moved as 16-byte pieces, or, in rows that no such piece divides,
+// eight values `stride` columns apart (neighbouring threads hold neighbouring
+// columns, so the loads of a warp stay whole).
+template <typename T> struct Raw {
   static constexpr int N = 8 * sizeof(T) / 16;
   uint4 r[N];
   __device__ __forceinline__ void clear() {
@@ -68,19 +72,24 @@ template <typename T> struct Raw<T, 8> {
 #pragma unroll
     for (int i = 0; i < N; i++) r[i] = reinterpret_cast<const uint4 *>(p)[i];
   }
-  // from an address with the element's alignment only
-  __device__ __forceinline__ void load_any(const T *p, bool vec) {
-    if (vec) {
-      load(p);
-    } else if constexpr (sizeof(T) == 4) {
-      const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
+  // values `stride` apart, zeros from the `left`-th column on
+  __device__ __forceinline__ void load_strided(const T *p, int stride, int left) {
+    using W = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
+    const W *q = reinterpret_cast<const W *>(p);
+    uint32_t v[8];
 #pragma unroll
-      for (int i = 0; i < N; i++) r[i] = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+    for (int i = 0; i < 8; i++) v[i] = i * stride < left ? q[i * stride] : 0u;
+    if constexpr (sizeof(T) == 4) {
+      r[0] = make_uint4(v[0], v[1], v[2], v[3]);
+      r[N - 1] = make_uint4(v[4], v[5], v[6], v[7]);
     } else {
-      const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
-      r[0] = make_uint4(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16,
-                        q[4] | (uint32_t)q[5] << 16, q[6] | (uint32_t)q[7] << 16);
+      r[0] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
+  }
+  // neighbours at an address with the element's alignment only
+  __device__ __forceinline__ void load_any(const T *p, bool vec) {
+    if (vec) load(p);
+    else load_strided(p, 1, 8);
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     constexpr int M = 8 / N;
@@ -99,68 +108,59 @@ template <typename T> struct Raw<T, 8> {
     for (int i = 0; i < 4; i++) f[i] = make_float2(g[2 * i], g[2 * i + 1]);
   }
 };
-template <typename T> struct Raw<T, 1> {
-  T r;
-  __device__ __forceinline__ void clear() { r = T(0.f); }
-  __device__ __forceinline__ void load(const T *p) { r = *p; }
-  __device__ __forceinline__ void load_shared(const T *p) { r = *p; }
-  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = io<T>::ld(&r); }
-};
 
-template <typename T, int V>
-__device__ __forceinline__ void ldv(const T *p, float (&f)[V]) {
-  Raw<T, V> r;
-  r.load(p);
-  r.get(f);
-}
-template <typename T, int V>
-__device__ __forceinline__ void stv(T *p, const float (&f)[V]) {
-  if constexpr (V == 1) {
-    io<T>::st(p, f[0]);
-  } else {
-    constexpr int N = fmap::vec16<T>::N;
+template <typename T>
+__device__ __forceinline__ void store8(T *p, const float (&f)[8]) {
+  constexpr int N = fmap::vec16<T>::N;
 #pragma unroll
-    for (int i = 0; i < V / N; i++) {
-      float g[N];
+  for (int i = 0; i < 8 / N; i++) {
+    float g[N];
 #pragma unroll
-      for (int j = 0; j < N; j++) g[j] = f[i * N + j];
-      fmap::st_stream(p + i * N, fmap::vec16<T>::pack(g));
-    }
+    for (int j = 0; j < N; j++) g[j] = f[i * N + j];
+    fmap::st_stream(p + i * N, fmap::vec16<T>::pack(g));
   }
 }
-// vec: the address is 16-byte aligned (else the element's alignment only)
 template <typename T>
-__device__ __forceinline__ void stv2(T *p, const float2 (&x)[4], bool vec) {
+__device__ __forceinline__ void store_strided(T *p, const float2 (&x)[4], int stride, int left) {
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    if (i * stride < left) io<T>::st(p + i * stride, i % 2 ? x[i / 2].y : x[i / 2].x);
+}
+template <typename T>
+__device__ __forceinline__ void store_pairs(T *p, const float2 (&x)[4]) {
   float f[8];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     f[2 * i] = x[i].x;
     f[2 * i + 1] = x[i].y;
   }
-  if (vec) {
-    stv<T, 8>(p, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; i++) io<T>::st(p + i, f[i]);
-  }
+  store8(p, f);
 }
-// Weights: fp32, read by every row of a CTA, so through the cache.
-template <int V>
-__device__ __forceinline__ void ldw(const float *w, int c, float (&f)[V]) {
+// vec: the address is 16-byte aligned (else the element's alignment only)
+template <typename T>
+__device__ __forceinline__ void store_any(T *p, const float2 (&x)[4], bool vec) {
+  if (vec) store_pairs(p, x);
+  else store_strided(p, x, 1, 8);
+}
+// Weights: fp32 (null: ones), read by every row of a CTA, so through the cache.
+__device__ __forceinline__ void weights8(const float *w, float2 (&f)[4]) {
   if (!w) {
 #pragma unroll
-    for (int i = 0; i < V; i++) f[i] = 1.f;
-  } else if constexpr (V == 1) {
-    f[0] = __ldg(w + c);
+    for (int i = 0; i < 4; i++) f[i] = make_float2(1.f, 1.f);
   } else {
+    const float4 x = __ldg(reinterpret_cast<const float4 *>(w)), y = __ldg(reinterpret_cast<const float4 *>(w) + 1);
+    f[0] = make_float2(x.x, x.y);
+    f[1] = make_float2(x.z, x.w);
+    f[2] = make_float2(y.x, y.y);
+    f[3] = make_float2(y.z, y.w);
+  }
+}
+__device__ __forceinline__ void weights_strided(const float *w, float2 (&f)[4], int stride, int left) {
 #pragma unroll
-    for (int i = 0; i < V / 4; i++) {
-      const float4 x = __ldg(reinterpret_cast<const float4 *>(w + c) + i);
-      f[4 * i] = x.x;
-      f[4 * i + 1] = x.y;
-      f[4 * i + 2] = x.z;
-      f[4 * i + 3] = x.w;
-    }
+  for (int i = 0; i < 8; i++) {
+    const float x = !w ? 1.f : i * stride < left ? __ldg(w + i * stride) : 0.f;
+    if (i % 2) f[i / 2].y = x;
+    else f[i / 2].x = x;
   }
 }
 __device__ __forceinline__ void copy(const float2 (&x)[4], float2 (&y)[4]) {
@@ -181,7 +181,7 @@ __device__ __forceinline__ void split_row(int64_t row, int64_t L, int64_t &b, in
 
 // ------------------------------------------------------------ pairs
 // Two fp32 operations in one instruction (each rounded as the single one is):
-// the backward of the gated norm is bound by the instructions it issues.
+// the norms' backward passes come near the rate at which instructions issue.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 a, b, d;\n\t"
@@ -348,15 +348,12 @@ gated_kernel(const __grid_constant__ Gated p) {
   int64_t at_o[NV];
   float2 held[HOLD ? NV : 1][P], acc[GRAD ? NV : 1][P];
   auto weights = [&](int col, float2 (&w)[P]) {
-    float f[V];
     if (col < end) {
-      ldw<V>(p.weight, p.shared ? col % e : col, f);
+      weights8(p.weight ? p.weight + (p.shared ? col % e : col) : nullptr, w);
     } else {
 #pragma unroll
-      for (int i = 0; i < V; i++) f[i] = 0.f;
+      for (int i = 0; i < P; i++) w[i] = pair(0.f);
     }
-#pragma unroll
-    for (int i = 0; i < P; i++) w[i] = make_float2(f[2 * i], f[2 * i + 1]);
   };
 #pragma unroll
   for (int n = 0; n < NV; n++) {
@@ -404,7 +401,7 @@ gated_kernel(const __grid_constant__ Gated p) {
     }
   };
   struct Loaded {
-    Raw<T, V> x[NV], g[GATE != GATE_NONE ? NV : 1], up[GRAD ? NV : 1];
+    Raw<T> x[NV], g[GATE != GATE_NONE ? NV : 1], up[GRAD ? NV : 1];
   };
   auto load = [&](Loaded &d, const Place &a) {
     const bool live = a.row < p.rows;
@@ -489,7 +486,7 @@ gated_kernel(const __grid_constant__ Gated p) {
             if constexpr (GATE != GATE_NONE) x[i] = mul2(x[i], sigmoid2<T>(g[i]));
             if constexpr (GATE == GATE_SILU) x[i] = mul2(x[i], g[i]);
           }
-          stv2(static_cast<T *>(p.u) + to.row * D + c[n], x, true);
+          store_pairs(static_cast<T *>(p.u) + to.row * D + c[n], x);
         } else {
           const float2 m = pair(-sum[n][1] * rstd.x * inv);  // -mean(dy * y)
           float2 up[P], dg[P];
@@ -509,9 +506,9 @@ gated_kernel(const __grid_constant__ Gated p) {
             acc[n][i] = fma2(uy, pair(1.f), acc[n][i]);
             x[i] = mul2(rstd, fma2(y, m, dy));
           }
-          stv2(static_cast<T *>(p.d_o) + to.o + at_o[n], x, true);
+          store_pairs(static_cast<T *>(p.d_o) + to.o + at_o[n], x);
           if constexpr (GATE != GATE_NONE)
-            stv2(static_cast<T *>(p.dgate) + to.dg + c[n], dg, p.dgate_vec);
+            store_any(static_cast<T *>(p.dgate) + to.dg + c[n], dg, p.dgate_vec);
         }
       }
     }
@@ -555,13 +552,17 @@ struct Residual {
   float *dw, *dpw;           // partial sums, or null
   int64_t rows;
   int D, cols, cl;           // columns, of a CTA; CTAs that share a row
+  int stages;                // rows that the ring holds (1 or 2)
   float alpha, beta, eps;
 };
 
-// Rows wider than a warp holds come through a ring of two rows in shared
-// memory, filled by thread 0 with one bulk copy per stream.  A row's stage is
-// given back by the block barrier of its first reduction, which no thread
-// passes before all have taken their values into registers.
+// Rows wider than a warp holds come through a ring of one or two rows in
+// shared memory, filled by thread 0 with one bulk copy per stream.  A row's
+// stage is given back by the block barrier of its first reduction, which no
+// thread passes before all have taken their values into registers; so even
+// one stage is filled again while its last row is worked on.  The weights
+// stand in front of the ring: with two CTAs on an SM little is left of the
+// L1 cache, and read from L2 for every row they cost as much as a stream.
 constexpr int kRingHead = 128;  // barriers and the flag, in front of the ring
 
 __device__ __forceinline__ void bulk_row(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -573,17 +574,19 @@ __device__ __forceinline__ void bulk_row(uint32_t dst, const void *src, uint32_t
 
 // The values of one row that a thread holds: forward h, y; backward h', dn,
 // dh', y (dh' and y where they are).
-template <typename T, typename R, bool GRAD, bool POST, int V, int NV>
+template <typename T, typename R, bool GRAD, bool POST, int NV>
 struct RowData {
-  Raw<R, V> h[NV], g[GRAD ? NV : 1];
-  Raw<T, V> s[GRAD ? NV : 1], y[(GRAD && !POST) ? 1 : NV];
+  Raw<R> h[NV], g[GRAD ? NV : 1];
+  Raw<T> s[GRAD ? NV : 1], y[(GRAD && !POST) ? 1 : NV];
 };
 
-template <typename T, typename R, bool GRAD, bool POST, int V, int NT, int TPR, int NV>
+// ONE: rows that no 16-byte piece divides (units of strided values).  TPR
+// threads hold a row, NV units of eight values each.
+template <typename T, typename R, bool GRAD, bool POST, bool ONE, int NT, int TPR, int NV>
 __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__ Residual p) {
-  constexpr bool RING = V == 8 && TPR > 32;
+  constexpr bool RING = !ONE && TPR > 32;
   constexpr bool HAS_Y = !GRAD || POST;  // y may be read
-  constexpr int RPC = NT / TPR;
+  constexpr int RPC = NT / TPR, P = 4;
   using Sum = RowSum<TPR, GRAD ? 3 : 1>;
   using Sum1 = RowSum<TPR, 1>;
   __shared__ typename Sum::Shared red;
@@ -598,17 +601,45 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
   const float inv = 1.f / (float)p.D;
   const T *y = static_cast<const T *>(p.y);
   const int64_t step = (int64_t)(gridDim.x / cl) * RPC;
-  int64_t r0 = (int64_t)(blockIdx.x / cl) * RPC;
+  const int64_t first = (int64_t)(blockIdx.x / cl) * RPC;
   if (cl > 1) cluster_arrive_wait();  // every CTA's shared memory is there
 
+  // unit n: its first column, and moves of its eight values
+  auto col = [&](int n) { return ONE ? n * 8 * TPR + tr : (n * TPR + tr) * 8; };
+  auto get = [&](auto &raw, const auto *row, int c) {
+    if constexpr (ONE) raw.load_strided(row + c, TPR, width - c);
+    else raw.load(row + c);
+  };
+  auto put = [&](auto *row, int c, const float2 (&x)[P]) {
+    if constexpr (ONE) store_strided(row + c, x, TPR, width - c);
+    else store_pairs(row + c, x);
+  };
+  // weights (0: w, 1: pw) of a unit.  In shared memory the first and the last
+  // four of each unit lie apart, so that a warp reads whole lines.
+  float4 *held = reinterpret_cast<float4 *>(dyn + kRingHead);
+  const int units = p.cols / 8;
+  auto weights = [&](int which, int c, float2 (&x)[P]) {
+    if constexpr (RING) {
+      const float4 a = held[2 * which * units + c / 8], b = held[(2 * which + 1) * units + c / 8];
+      x[0] = make_float2(a.x, a.y);
+      x[1] = make_float2(a.z, a.w);
+      x[2] = make_float2(b.x, b.y);
+      x[3] = make_float2(b.z, b.w);
+    } else {
+      const float *w = which ? p.post_weight : p.weight;
+      if constexpr (ONE) weights_strided(w ? w + c0 + c : w, x, TPR, width - c);
+      else weights8(w ? w + c0 + c : w, x);
+    }
+  };
+
+  // a stage of the ring: h | dh' | dn | y, the ones that are
   const uint32_t hb = (uint32_t)width * sizeof(R), yb = (uint32_t)width * sizeof(T);
   const bool has_g = GRAD && p.dh_new, has_y = HAS_Y && y;
   const uint32_t bars = smem_u32(dyn);
   volatile int *abort = reinterpret_cast<volatile int *>(dyn + 64);
-  // a stage: h | g | s | y, the ones that are
   const uint32_t at_g = hb, at_s = at_g + (has_g ? hb : 0), at_y = at_s + (GRAD ? yb : 0);
   const uint32_t row_bytes = at_y + (has_y ? yb : 0), stage_bytes = (row_bytes + 127) / 128 * 128;
-  char *ring = dyn + kRingHead;
+  char *ring = dyn + kRingHead + (POST ? 2 : 1) * sizeof(float) * p.cols;
   auto fetch = [&](int64_t row, int st) {  // thread 0
     const uint32_t bar = bars + st * 8, dst = smem_u32(ring) + st * stage_bytes;
     const int64_t at = row * p.D + c0;
@@ -627,35 +658,48 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-      if (r0 < p.rows) fetch(r0, 0);
-      if (r0 + step < p.rows) fetch(r0 + step, 1);
+      if (first < p.rows) fetch(first, 0);
+      if (p.stages > 1 && first + step < p.rows) fetch(first + step, 1);
     }
+    for (int i = threadIdx.x; i < (POST ? 2 : 1) * units; i += NT) {
+      const int which = i >= units, u = i - which * units;
+      const float *w = which ? p.post_weight : p.weight;
+      if (u * 8 < width) {
+        float2 x[P];
+        weights8(w ? w + c0 + u * 8 : w, x);
+        held[2 * which * units + u] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+        held[(2 * which + 1) * units + u] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+      }
+    }
+    __syncthreads();
   }
+  const int shift = p.stages - 1;
 
-  float aw[GRAD ? NV : 1][V], ap[GRAD && POST ? NV : 1][V];
+  float2 aw[GRAD ? NV : 1][P], ap[GRAD && POST ? NV : 1][P];
   if constexpr (GRAD) {
 #pragma unroll
     for (int n = 0; n < NV; n++)
 #pragma unroll
-      for (int i = 0; i < V; i++) {
-        aw[n][i] = 0.f;
-        if constexpr (POST) ap[n][i] = 0.f;
+      for (int i = 0; i < P; i++) {
+        aw[n][i] = pair(0.f);
+        if constexpr (POST) ap[n][i] = pair(0.f);
       }
   }
 
-  for (int64_t it = 0; r0 < p.rows; r0 += step, it++) {
+  int64_t it = 0;
+  for (int64_t r0 = first; r0 < p.rows; r0 += step, it++) {
     const int64_t row = r0 + sub;
     const bool live = row < p.rows;
     const int64_t at = row * p.D + c0;
-    RowData<T, R, GRAD, POST, V, NV> d;
-    const int st = (int)(it & 1);
+    RowData<T, R, GRAD, POST, NV> d;
+    const int st = (int)it & shift;
     const char *stage = ring + st * stage_bytes;
     // on a timeout the values are stale, but every thread stays in step with
     // the barriers below; the error word tells the host
-    if constexpr (RING) mbar_wait(bars + st * 8, (uint32_t)(it >> 1) & 1, abort);
+    if constexpr (RING) mbar_wait(bars + st * 8, (uint32_t)(it >> shift) & 1, abort);
 #pragma unroll
     for (int n = 0; n < NV; n++) {
-      const int c = (n * TPR + tr) * V;
+      const int c = col(n);
       if (live && c < width) {
         if constexpr (RING) {
           d.h[n].load_shared(reinterpret_cast<const R *>(stage) + c);
@@ -668,14 +712,14 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
             if (has_y) d.y[n].load_shared(reinterpret_cast<const T *>(stage + at_y) + c);
           }
         } else {
-          d.h[n].load(static_cast<const R *>(p.h) + at + c);
+          get(d.h[n], static_cast<const R *>(p.h) + at, c);
           if constexpr (GRAD) {
-            if (has_g) d.g[n].load(static_cast<const R *>(p.dh_new) + at + c);
+            if (has_g) get(d.g[n], static_cast<const R *>(p.dh_new) + at, c);
             else d.g[n].clear();
-            d.s[n].load(static_cast<const T *>(p.dn) + at + c);
+            get(d.s[n], static_cast<const T *>(p.dn) + at, c);
           }
           if constexpr (HAS_Y) {
-            if (has_y) d.y[n].load(y + at + c);
+            if (has_y) get(d.y[n], y + at, c);
           }
         }
       } else {
@@ -690,138 +734,147 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
     // after the row's first barrier: its stage is free
     auto refill = [&] {
       if constexpr (RING) {
-        if (threadIdx.x == 0 && r0 + 2 * step < p.rows) fetch(r0 + 2 * step, st);
+        const int64_t later = r0 + p.stages * step;
+        if (threadIdx.x == 0 && later < p.rows) fetch(later, st);
       }
     };
     if constexpr (!GRAD) {
-      float x[NV][V];
+      float2 x[NV][P];
       bool refilled = false;
 #pragma unroll
-      for (int n = 0; n < NV; n++) d.h[n].get(x[n]);
+      for (int n = 0; n < NV; n++) d.h[n].get2(x[n]);
       if (y) {
-        float ry = 1.f;
+        float2 ry = pair(p.beta);
         if constexpr (POST) {
-          float q[1] = {0.f};
+          float2 q2 = pair(0.f);
 #pragma unroll
           for (int n = 0; n < NV; n++) {
-            float z[V];
-            d.y[n].get(z);
+            float2 z[P];
+            d.y[n].get2(z);
 #pragma unroll
-            for (int i = 0; i < V; i++) q[0] = fmaf(z[i], z[i], q[0]);
+            for (int i = 0; i < P; i++) q2 = fma2(z[i], z[i], q2);
           }
+          float q[1] = {q2.x + q2.y};
           sum1(q, red1, cl, rank);
           refill();
           refilled = true;
-          ry = rsqrtf(fmaf(q[0], inv, p.eps));
+          ry = pair(rsqrtf(fmaf(q[0], inv, p.eps)) * p.beta);
         }
+        const float2 al = pair(p.alpha);
 #pragma unroll
         for (int n = 0; n < NV; n++) {
-          const int c = (n * TPR + tr) * V;
+          const int c = col(n);
           if (!(live && c < width)) continue;
-          float z[V], w[V];
-          d.y[n].get(z);
-          if constexpr (POST) ldw<V>(p.post_weight, c0 + c, w);
+          float2 z[P], w[P];
+          d.y[n].get2(z);
+          if constexpr (POST) weights(1, c, w);
 #pragma unroll
-          for (int i = 0; i < V; i++) {
-            const float q = POST ? z[i] * ry * w[i] : z[i];
-            x[n][i] = fmaf(p.beta, q, p.alpha * x[n][i]);
+          for (int i = 0; i < P; i++) {
+            if constexpr (POST) z[i] = mul2(z[i], w[i]);
+            x[n][i] = fma2(ry, z[i], mul2(al, x[n][i]));
           }
-          stv<R, V>(static_cast<R *>(p.h_new) + at + c, x[n]);
+          put(static_cast<R *>(p.h_new) + at, c, x[n]);
         }
       }
-      float q[1] = {0.f};
+      float2 q2 = pair(0.f);
 #pragma unroll
       for (int n = 0; n < NV; n++)
 #pragma unroll
-        for (int i = 0; i < V; i++) q[0] = fmaf(x[n][i], x[n][i], q[0]);
+        for (int i = 0; i < P; i++) q2 = fma2(x[n][i], x[n][i], q2);
+      float q[1] = {q2.x + q2.y};
       sum(q, red, cl, rank);
       if (!refilled) refill();
-      const float rstd = rsqrtf(fmaf(q[0], inv, p.eps));
+      const float2 rstd = pair(rsqrtf(fmaf(q[0], inv, p.eps)));
 #pragma unroll
       for (int n = 0; n < NV; n++) {
-        const int c = (n * TPR + tr) * V;
+        const int c = col(n);
         if (!(live && c < width)) continue;
-        float w[V];
-        ldw<V>(p.weight, c0 + c, w);
+        float2 w[P];
+        weights(0, c, w);
 #pragma unroll
-        for (int i = 0; i < V; i++) w[i] *= x[n][i] * rstd;
-        stv<T, V>(static_cast<T *>(p.n) + at + c, w);
+        for (int i = 0; i < P; i++) w[i] = mul2(w[i], mul2(x[n][i], rstd));
+        put(static_cast<T *>(p.n) + at, c, w);
       }
     } else {
       // sums of h'^2, (dn w) h' and, with a norm on y, y^2
-      float q[3] = {0.f, 0.f, 0.f};
+      float2 q0 = pair(0.f), q1 = pair(0.f), q2 = pair(0.f);
 #pragma unroll
       for (int n = 0; n < NV; n++) {
-        const int c = (n * TPR + tr) * V;
+        const int c = col(n);
         if (c >= width) continue;
-        float w[V], x[V], s[V];
-        ldw<V>(p.weight, c0 + c, w);
-        d.h[n].get(x);
-        d.s[n].get(s);
+        float2 w[P], x[P], s[P];
+        weights(0, c, w);
+        d.h[n].get2(x);
+        d.s[n].get2(s);
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-          q[0] = fmaf(x[i], x[i], q[0]);
-          q[1] = fmaf(s[i] * w[i], x[i], q[1]);
+        for (int i = 0; i < P; i++) {
+          q0 = fma2(x[i], x[i], q0);
+          q1 = fma2(mul2(s[i], w[i]), x[i], q1);
         }
         if constexpr (POST) {
-          float z[V];
-          d.y[n].get(z);
+          float2 z[P];
+          d.y[n].get2(z);
 #pragma unroll
-          for (int i = 0; i < V; i++) q[2] = fmaf(z[i], z[i], q[2]);
+          for (int i = 0; i < P; i++) q2 = fma2(z[i], z[i], q2);
         }
       }
+      float q[3] = {q0.x + q0.y, q1.x + q1.y, q2.x + q2.y};
       sum(q, red, cl, rank);
       refill();
-      const float rstd = rsqrtf(fmaf(q[0], inv, p.eps));
-      const float m = q[1] * rstd * inv;  // mean(s hn)
-      const float ry = POST ? rsqrtf(fmaf(q[2], inv, p.eps)) : 1.f;
-      float k[1] = {0.f};                 // sum of (dp pw) yn
-      float dp[NV][V];
+      const float r = rsqrtf(fmaf(q[0], inv, p.eps));
+      const float2 rstd = pair(r), m = pair(-q[1] * r * inv);  // -mean(s hn)
+      const float2 ry = pair(POST ? rsqrtf(fmaf(q[2], inv, p.eps)) : 1.f);
+      const float2 al = pair(p.alpha), be = pair(p.beta);
+      float2 k = pair(0.f), dp[NV][P];       // k: sum of (dp pw) yn
 #pragma unroll
       for (int n = 0; n < NV; n++) {
-        const int c = (n * TPR + tr) * V;
+        const int c = col(n);
         if (!(live && c < width)) continue;
-        float w[V], x[V], s[V], g[V];
-        ldw<V>(p.weight, c0 + c, w);
-        d.h[n].get(x);
-        d.s[n].get(s);
-        d.g[n].get(g);
+        float2 w[P], x[P], s[P], g[P];
+        weights(0, c, w);
+        d.h[n].get2(x);
+        d.s[n].get2(s);
+        d.g[n].get2(g);
 #pragma unroll
-        for (int i = 0; i < V; i++) {
-          const float hn = x[i] * rstd;
-          aw[n][i] = fmaf(s[i], hn, aw[n][i]);
-          const float dH = fmaf(rstd, fmaf(-hn, m, s[i] * w[i]), g[i]);
-          x[i] = p.alpha * dH;
-          dp[n][i] = p.beta * dH;
+        for (int i = 0; i < P; i++) {
+          const float2 hn = mul2(x[i], rstd);
+          aw[n][i] = fma2(s[i], hn, aw[n][i]);
+          const float2 dH = fma2(rstd, fma2(hn, m, mul2(s[i], w[i])), g[i]);
+          x[i] = mul2(al, dH);
+          dp[n][i] = mul2(be, dH);
         }
-        stv<R, V>(static_cast<R *>(p.dh) + at + c, x);
+        put(static_cast<R *>(p.dh) + at, c, x);
         if constexpr (POST) {
-          float z[V];
-          d.y[n].get(z);
-          ldw<V>(p.post_weight, c0 + c, w);
+          float2 z[P];
+          d.y[n].get2(z);
+          weights(1, c, w);
 #pragma unroll
-          for (int i = 0; i < V; i++) {
-            const float yn = z[i] * ry;
-            ap[n][i] = fmaf(dp[n][i], yn, ap[n][i]);
-            dp[n][i] *= w[i];
-            k[0] = fmaf(dp[n][i], yn, k[0]);
+          for (int i = 0; i < P; i++) {
+            const float2 yn = mul2(z[i], ry);
+            ap[n][i] = fma2(dp[n][i], yn, ap[n][i]);
+            dp[n][i] = mul2(dp[n][i], w[i]);
+            k = fma2(dp[n][i], yn, k);
           }
         }
       }
       if (p.dy) {
-        if constexpr (POST) sum1(k, red1, cl, rank);
-        const float mz = k[0] * inv;
+        float2 mz = pair(0.f);               // -mean((dp pw) yn) / rms(y)
+        if constexpr (POST) {
+          float t[1] = {k.x + k.y};
+          sum1(t, red1, cl, rank);
+          mz = mul2(pair(-t[0] * inv), ry);
+        }
 #pragma unroll
         for (int n = 0; n < NV; n++) {
-          const int c = (n * TPR + tr) * V;
+          const int c = col(n);
           if (!(live && c < width)) continue;
           if constexpr (POST) {
-            float z[V];
-            d.y[n].get(z);
+            float2 z[P];
+            d.y[n].get2(z);
 #pragma unroll
-            for (int i = 0; i < V; i++) dp[n][i] = ry * fmaf(-z[i] * ry, mz, dp[n][i]);
+            for (int i = 0; i < P; i++) dp[n][i] = mul2(ry, fma2(z[i], mz, dp[n][i]));
           }
-          stv<T, V>(static_cast<T *>(p.dy) + at + c, dp[n]);
+          put(static_cast<T *>(p.dy) + at, c, dp[n]);
         }
       }
     }
@@ -830,47 +883,42 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
     // after a timeout: let the rows in flight land before the ring is released
     if (threadIdx.x == 0 && *abort) {
       volatile int none = 0;
-      const int64_t n = (p.rows - (int64_t)(blockIdx.x / cl) + step - 1) / step;  // rows fetched
-      for (int64_t j = n > 2 ? n - 2 : 0; j < n; j++)
-        mbar_wait(bars + (uint32_t)(j & 1) * 8, (uint32_t)(j >> 1) & 1, &none);
+      for (int64_t j = it > p.stages ? it - p.stages : 0; j < it; j++)
+        mbar_wait(bars + ((uint32_t)j & shift) * 8, (uint32_t)(j >> shift) & 1, &none);
     }
   }
   if constexpr (GRAD) {
     launch_dependents();
     // one row of partial sums for the CTA's columns; warps that walked rows
     // side by side are added up first
-    float *out[2] = {p.dw, POST ? p.dpw : nullptr};
     const int64_t group = blockIdx.x / cl;
-#pragma unroll
-    for (int j = 0; j < (POST ? 2 : 1); j++) {
-      if (!out[j]) continue;
-      float *to = out[j] + group * p.D + c0;
+    auto flush = [&](float *to, const float2 (&acc)[NV][P]) {
+      if (!to) return;
+      to += group * p.D + c0;
       if constexpr (RPC == 1) {
 #pragma unroll
         for (int n = 0; n < NV; n++) {
-          const int c = (n * TPR + tr) * V;
-          if (c < width) {
-#pragma unroll
-            for (int i = 0; i < V; i++) to[c + i] = j ? ap[POST ? n : 0][i] : aw[n][i];
-          }
+          const int c = col(n);
+          if (c < width) put(to, c, acc[n]);
         }
       } else {
-        float *acc_s = reinterpret_cast<float *>(dyn);
+        float2 *acc_s = reinterpret_cast<float2 *>(dyn);
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < NV; n++)
 #pragma unroll
-          for (int i = 0; i < V; i++)
-            acc_s[sub * (TPR * NV * V) + (n * TPR + tr) * V + i] = j ? ap[POST ? n : 0][i] : aw[n][i];
+          for (int i = 0; i < P; i++) acc_s[(sub * NV * TPR + n * TPR + tr) * P + i] = acc[n][i];
         __syncthreads();
         for (int c = threadIdx.x; c < width; c += NT) {
           float a = 0.f;
 #pragma unroll
-          for (int r = 0; r < RPC; r++) a += acc_s[r * (TPR * NV * V) + c];
+          for (int k = 0; k < RPC; k++) a += reinterpret_cast<float *>(dyn)[k * (TPR * NV * 8) + c];
           to[c] = a;
         }
       }
-    }
+    };
+    flush(p.dw, aw);
+    if constexpr (POST) flush(p.dpw, ap);
   }
 }
 

@@ -29,6 +29,19 @@ constexpr int NT = 256;   // threads per CTA
 constexpr int TOK = 4;    // tokens per CTA
 constexpr int LANES = NT / TOK;
 
+// V values of T as they are in memory.
+template <typename T, int V> struct Unit : norm::Raw<T> {};
+template <typename T> struct Unit<T, 1> {
+  T r;
+  __device__ __forceinline__ void load(const T *p) { r = *p; }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = io<T>::ld(&r); }
+};
+template <typename T, int V>
+__device__ __forceinline__ void put(T *p, const float (&f)[V]) {
+  if constexpr (V == 1) io<T>::st(p, f[0]);
+  else norm::store8(p, f);
+}
+
 // One tensor: `n` heads of `width` columns on the strided side (strides in
 // values, unit column stride), n * rep heads on the head-major side.
 struct Part {
@@ -78,7 +91,7 @@ __global__ void __launch_bounds__(NT, 3) rotary_kernel(const __grid_constant__ A
     T *major = static_cast<T *>(p.major) + (b * p.n * rep * a.L + t) * p.width;
     const int h0 = blockIdx.y * per + lane / chunks, stride = gridDim.y * per;
     const int n = live ? p.n : 0;
-    norm::Raw<T, V> x0[U], x1[U];
+    Unit<T, V> x0[U], x1[U];
     auto fetch = [&](int h) {
 #pragma unroll
       for (int u = 0; u < U; u++) {
@@ -147,14 +160,14 @@ __global__ void __launch_bounds__(NT, 3) rotary_kernel(const __grid_constant__ A
           x1[u].get(g);
           turn(f, g);
           if constexpr (GRAD) {
-            norm::stv<T, V>(strided + hu * p.sh + c0, f);
-            norm::stv<T, V>(strided + hu * p.sh + c1, g);
+            put<T, V>(strided + hu * p.sh + c0, f);
+            put<T, V>(strided + hu * p.sh + c1, g);
           } else {
             T *m = major + (int64_t)hu * rep * hstep;
 #pragma unroll 1
             for (int j = 0; j < rep; j++, m += hstep) {
-              norm::stv<T, V>(m + c0, f);
-              norm::stv<T, V>(m + c1, g);
+              put<T, V>(m + c0, f);
+              put<T, V>(m + c1, g);
             }
           }
         }
@@ -188,8 +201,8 @@ __global__ void __launch_bounds__(NT, 3) rotary_kernel(const __grid_constant__ A
           }
         }
         turn(f, g);
-        norm::stv<T, V>(strided + h * p.sh + c0, f);
-        norm::stv<T, V>(strided + h * p.sh + c1, g);
+        put<T, V>(strided + h * p.sh + c0, f);
+        put<T, V>(strided + h * p.sh + c1, g);
       }
     }
   }
