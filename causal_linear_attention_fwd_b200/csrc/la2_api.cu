@@ -636,10 +636,10 @@ struct NormPlan {
 // The row's width decides who holds it (see la2_norm.cuh): a warp, a CTA with
 // one or two vectors per thread, or a cluster of CTAs.  `one` values at a time
 // where no 16-byte piece divides the row.
-NormPlan row_plan(int D, bool one) {
+NormPlan row_plan(int D, bool one, int most_units = 2) {
   NormPlan g;
   g.slices = 1;
-  const int most = one ? 2048 : 4096;
+  const int most = one ? 2048 : 2048 * most_units;
   g.cl = 1;
   while (g.cl * most < D) g.cl *= 2;
   const int unit = one ? 1 : 8;
@@ -650,7 +650,7 @@ NormPlan row_plan(int D, bool one) {
     g.nv = 2;
   } else {
     g.nt = g.tpr = 256;
-    g.nv = one || g.cols <= 2048 ? 1 : 2;
+    g.nv = one || g.cols <= 2048 ? 1 : g.cols <= 4096 ? 2 : 4;
   }
   g.rpc = g.nt / g.tpr;
   return g;
@@ -734,7 +734,9 @@ cudaError_t launch_groups(K kern, const P &p, const NormPlan &g, int64_t groups,
 template <typename T, int E, bool ROW, bool GRAD, la2::norm::Gate GATE, int NT, int TPR, int NV>
 cudaError_t gated_launch(la2::norm::Gated p, const NormPlan &g, float *dw, cudaStream_t st) {
   auto kern = la2::norm::gated_kernel<T, E, ROW, GRAD, GATE, NT, TPR, NV>;
-  constexpr size_t smem = GRAD ? (size_t)NT * NV * 8 * sizeof(float) : 0;
+  constexpr size_t smem = la2::norm::gated_smem<T, GRAD, GATE, NT, NV>();
+  if (smem > 32 * 1024)  // 48 KB with the static arrays go without
+    if (cudaError_t e = opt_in_smem(kern, smem)) return e;
   static std::atomic<uint64_t> last{0};
   const int per_sm = resident(kern, NT, smem, last);
   const int64_t groups =
@@ -795,7 +797,7 @@ cudaError_t residual_launch(la2::norm::Residual p, const NormPlan &g, float *dw,
   } else if (GRAD && TPR == 32) {
     smem = (size_t)NT * NV * 8 * sizeof(float);
   }
-  if (smem > 48 * 1024)
+  if (smem > 32 * 1024)  // 48 KB with the static arrays go without
     if (cudaError_t e = opt_in_smem(kern, smem)) return e;
   static std::atomic<uint64_t> last{0};
   int per_sm = resident(kern, NT, smem, last);
@@ -814,10 +816,12 @@ cudaError_t residual_launch(la2::norm::Residual p, const NormPlan &g, float *dw,
 template <typename T, typename R, bool POST, bool GRAD>
 cudaError_t residual_shape(const la2::norm::Residual &p, float *dw, float *dpw, cudaStream_t st) {
   const bool one = p.D % 8 != 0;
-  const NormPlan g = row_plan(p.D, one);
+  const NormPlan g = row_plan(p.D, one, GRAD ? 2 : 4);
   if (one) return residual_launch<T, R, POST, GRAD, true, 256, 256, 1>(p, g, dw, dpw, st);
   if (g.tpr == 32) return residual_launch<T, R, POST, GRAD, false, 128, 32, 2>(p, g, dw, dpw, st);
   if (g.nv == 1) return residual_launch<T, R, POST, GRAD, false, 256, 256, 1>(p, g, dw, dpw, st);
+  if constexpr (!GRAD)
+    if (g.nv == 4) return residual_launch<T, R, POST, GRAD, false, 256, 256, 4>(p, g, dw, dpw, st);
   return residual_launch<T, R, POST, GRAD, false, 256, 256, 2>(p, g, dw, dpw, st);
 }
 

@@ -25,9 +25,9 @@
 // registers across the row's reductions, and the backward needs no saved
 // statistics because the row it must read anyway gives them again.  While a
 // row is reduced and written the next one is on its way: the gated norm
-// (rows made of 128- or 256-byte pieces of the heads) loads it into
-// registers, the residual norm (contiguous rows) by bulk copies into a ring
-// of rows in shared memory.
+// (rows made of 128- or 256-byte pieces of the heads) has each thread copy its
+// own next values into shared memory, the residual norm (contiguous rows)
+// takes them by bulk copies into a ring of rows there.
 //
 // A row is held by a warp (up to 512 columns), a CTA (up to 4,096; 2,048 where
 // values move one by one) or a cluster of 2 to 8 CTAs that add their partial
@@ -141,6 +141,15 @@ template <typename T>
 __device__ __forceinline__ void store_any(T *p, const float2 (&x)[4], bool vec) {
   if (vec) store_pairs(p, x);
   else store_strided(p, x, 1, 8);
+}
+// 16 bytes into shared memory, behind the thread's back.
+__device__ __forceinline__ void copy16_async(void *to, const void *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 // Weights: fp32 (null: ones), read by every row of a CTA, so through the cache.
 __device__ __forceinline__ void weights8(const float *w, float2 (&f)[4]) {
@@ -279,24 +288,18 @@ __device__ __forceinline__ void launch_dependents() {
 }
 
 // ------------------------------------------------------------ gate
-// 1 / (1 + e^-g) of a pair.  e^-g overflows to infinity for g below -88,
-// where the sigmoid is 0 to fp32 (the quotient gives it).  Values that will
-// be rounded to bf16 take the approximate exponential (of base 2) and
-// reciprocal, a few 2^-23 off against the rounding's 2^-9; fp32 takes the
-// exact ones.
-template <typename T>
+// 1 / (1 + e^-g) of a pair, by the approximate exponential (of base 2) and
+// reciprocal: relative error below (|g| + 4) 2^-23, from the exponent's
+// rounding.  e^-g overflows to infinity for g below -88, where the sigmoid is
+// 0 to fp32 (the reciprocal gives it).
 __device__ __forceinline__ float2 sigmoid2(float2 g) {
-  if constexpr (sizeof(T) == 4) {
-    return make_float2(1.f / (1.f + expf(-g.x)), 1.f / (1.f + expf(-g.y)));
-  } else {
-    float2 s = mul2(g, pair(-1.44269504f));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(s.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(s.y));
-    s = fma2(s, pair(1.f), pair(1.f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(s.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(s.y));
-    return s;
-  }
+  float2 s = mul2(g, pair(-1.44269504f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(s.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(s.y));
+  s = fma2(s, pair(1.f), pair(1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(s.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(s.y));
+  return s;
 }
 
 // ------------------------------------------------------------ gated norm
@@ -318,20 +321,34 @@ struct Gated {
   float eps;
 };
 
+// Rows on their way per thread, and CTAs on an SM.
+template <bool GRAD, Gate GATE>
+constexpr int gated_streams() { return 1 + GRAD + (GATE != GATE_NONE); }
+template <typename T, int NV>
+constexpr int gated_stages() { return NV == 2 ? 2 : 3; }
+template <typename T, bool GRAD, int NV>
+constexpr int gated_ctas() { return GRAD || sizeof(T) == 4 ? 2 : 4; }
+template <typename T, bool GRAD, Gate GATE, int NT, int NV>
+constexpr size_t gated_smem() {
+  const size_t ring = (size_t)NT * NV * 8 * sizeof(T) * gated_streams<GRAD, GATE>() * gated_stages<T, NV>();
+  const size_t sums = GRAD ? (size_t)NT * NV * 8 * sizeof(float) : 0;  // in its place, at the end
+  return ring > sums ? ring : sums;
+}
+
 // ROW: one norm spans the H * e values of a token (else one per head, of E =
 // e columns; a row's kernel takes every e, its E is 0).
 // Threads of a CTA: per head, 2^tpr_shift side by side over `cols` columns
 // (heads; slice blockIdx.y) and NT >> tpr_shift tokens; ROW, a warp or the
 // CTA per row, NV vectors each, slice = the CTA's rank in its cluster.
 template <typename T, int E, bool ROW, bool GRAD, Gate GATE, int NT, int TPR, int NV>
-__global__ void __launch_bounds__(NT, GRAD || sizeof(T) == 4 ? 2 : 3)
+__global__ void __launch_bounds__(NT, gated_ctas<T, GRAD, NV>())
 gated_kernel(const __grid_constant__ Gated p) {
   constexpr int V = 8, P = V / 2, LPH = ROW ? 32 : E / V;
-  // what fits the registers: the next row ahead, the weights held throughout
-  constexpr bool AHEAD = !(GRAD && NV == 2 && sizeof(T) == 4), HOLD = !(GRAD && NV == 2);
+  constexpr int S = gated_stages<T, NV>();
+  constexpr bool HOLD = !(GRAD && NV == 2);  // the weights, in registers throughout
   using Sum = RowSum<ROW ? TPR : 32, GRAD ? 2 : 1>;
   __shared__ typename Sum::Shared red;
-  extern __shared__ float acc_s[];
+  extern __shared__ __align__(128) char dyn[];
   Sum row_sum;
   const int cl = ROW ? p.cl : 1;
   const int rank = ROW && TPR > 32 && cl > 1 ? (int)cluster_rank() : 0;
@@ -400,32 +417,69 @@ gated_kernel(const __grid_constant__ Gated p) {
       if constexpr (GRAD) a.dg += wrap_dg;
     }
   };
-  struct Loaded {
-    Raw<T> x[NV], g[GATE != GATE_NONE ? NV : 1], up[GRAD ? NV : 1];
+  // The rows ahead: this thread's vectors of each stream (o, the gate, du) in
+  // its own places of shared memory, so it alone waits for them and no
+  // barrier is needed.  Lanes stand 16 bytes apart.
+  constexpr int N = Raw<T>::N, STREAMS = gated_streams<GRAD, GATE>();
+  const bool gate_ahead = GATE != GATE_NONE && p.gate_vec;
+  auto slot = [&](int stage, int stream, int n, int i) {
+    return reinterpret_cast<uint4 *>(dyn) + (((stage * STREAMS + stream) * NV + n) * N + i) * NT + threadIdx.x;
   };
-  auto load = [&](Loaded &d, const Place &a) {
-    const bool live = a.row < p.rows;
+  auto fetch = [&](int stage, const Place &a) {
+    if (a.row < p.rows) {
+#pragma unroll
+      for (int n = 0; n < NV; n++) {
+        if (c[n] >= end) continue;
+        const T *x = static_cast<const T *>(p.o) + a.o + at_o[n];
+        const T *g = static_cast<const T *>(p.gate) + a.g + c[n];
+        const T *up = static_cast<const T *>(p.du) + a.row * D + c[n];
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+          copy16_async(slot(stage, 0, n, i), reinterpret_cast<const uint4 *>(x) + i);
+          if (GRAD) copy16_async(slot(stage, 1, n, i), reinterpret_cast<const uint4 *>(up) + i);
+          if (gate_ahead) copy16_async(slot(stage, STREAMS - 1, n, i), reinterpret_cast<const uint4 *>(g) + i);
+        }
+      }
+    }
+    copies_commit();
+  };
+  struct {
+    Raw<T> x[NV], g[GATE != GATE_NONE ? NV : 1], up[GRAD ? NV : 1];
+  } cur;
+  auto take = [&](int stage, const Place &a) {
 #pragma unroll
     for (int n = 0; n < NV; n++) {
-      if (live && c[n] < end) {
-        d.x[n].load(static_cast<const T *>(p.o) + a.o + at_o[n]);
+      if (a.row < p.rows && c[n] < end) {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+          cur.x[n].r[i] = *slot(stage, 0, n, i);
+          if constexpr (GRAD) cur.up[n].r[i] = *slot(stage, 1, n, i);
+          if constexpr (GATE != GATE_NONE)
+            if (gate_ahead) cur.g[n].r[i] = *slot(stage, STREAMS - 1, n, i);
+        }
         if constexpr (GATE != GATE_NONE)
-          d.g[n].load_any(static_cast<const T *>(p.gate) + a.g + c[n], p.gate_vec);
-        if constexpr (GRAD) d.up[n].load(static_cast<const T *>(p.du) + a.row * D + c[n]);
+          if (!gate_ahead) cur.g[n].load_any(static_cast<const T *>(p.gate) + a.g + c[n], false);
       } else {
-        d.x[n].clear();
-        if constexpr (GATE != GATE_NONE) d.g[n].clear();
-        if constexpr (GRAD) d.up[n].clear();
+        cur.x[n].clear();
+        if constexpr (GATE != GATE_NONE) cur.g[n].clear();
+        if constexpr (GRAD) cur.up[n].clear();
       }
     }
   };
-  Loaded cur, next;
-  Place to = at;  // of the row at hand; `at` is the next one's
-  if (AHEAD) load(cur, at);
-  for (int64_t r = r0; r < p.rows; r += step) {
+  Place to = at;  // of the row at hand; `at` is S - 1 rows on
+#pragma unroll
+  for (int i = 0; i < S - 1; i++) {
+    fetch(i, at);
     advance(at);
-    if constexpr (AHEAD) load(next, at);
-    else load(cur, to);
+  }
+  int stage = 0, last = S - 1;
+  for (int64_t r = r0; r < p.rows; r += step) {
+    fetch(last, at);
+    advance(at);
+    copies_wait<S - 1>();
+    take(stage, to);
+    last = stage;
+    stage = stage + 1 == S ? 0 : stage + 1;
     // statistics of the row or head; in the backward also sum(dy * o)
     float2 s[GRAD && GATE != GATE_NONE ? NV : 1][P];
     float sum[NV][GRAD ? 2 : 1];
@@ -445,7 +499,7 @@ gated_kernel(const __grid_constant__ Gated p) {
         if constexpr (GRAD) {
           float2 dy = mul2(up[i], w[i]);
           if constexpr (GATE != GATE_NONE) {
-            s[n][i] = sigmoid2<T>(g[i]);
+            s[n][i] = sigmoid2(g[i]);
             dy = mul2(dy, s[n][i]);
           }
           if constexpr (GATE == GATE_SILU) dy = mul2(dy, g[i]);
@@ -483,7 +537,7 @@ gated_kernel(const __grid_constant__ Gated p) {
 #pragma unroll
           for (int i = 0; i < P; i++) {
             x[i] = mul2(mul2(x[i], rstd), w[i]);
-            if constexpr (GATE != GATE_NONE) x[i] = mul2(x[i], sigmoid2<T>(g[i]));
+            if constexpr (GATE != GATE_NONE) x[i] = mul2(x[i], sigmoid2(g[i]));
             if constexpr (GATE == GATE_SILU) x[i] = mul2(x[i], g[i]);
           }
           store_pairs(static_cast<T *>(p.u) + to.row * D + c[n], x);
@@ -512,12 +566,14 @@ gated_kernel(const __grid_constant__ Gated p) {
         }
       }
     }
-    if constexpr (AHEAD) cur = next;
-    to = at;
+    advance(to);
   }
   if constexpr (GRAD) {
     if (!p.dw) return;
     launch_dependents();
+    float *acc_s = reinterpret_cast<float *>(dyn);
+    copies_wait<0>();
+    __syncthreads();
     // the CTA's partial sums: over the tokens side by side and, for a weight
     // that the heads share, over the heads it covers
 #pragma unroll
