@@ -229,54 +229,80 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void store_in_cta(float *p, uint32_t rank, float x) {
+// One value into the shared memory of CTA `rank`, counted by the barrier at
+// the same place there.
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, uint32_t rank, float x) {
   asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(smem_u32(p)),
-      "r"(rank), "f"(x)
+      "{\n\t.reg .b32 a, b;\n\t"
+      "mapa.shared::cluster.u32 a, %0, %2;\n\t"
+      "mapa.shared::cluster.u32 b, %1, %2;\n\t"
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [a], %3, [b];\n\t}" ::"r"(to),
+      "r"(bar), "r"(rank), "f"(x)
       : "memory");
 }
 
 // Sum of K values over the threads that share a row: a warp (TPR = 32), the
-// CTA (cl = 1) or the cl CTAs of a cluster, each of which is given all warps'
+// CTA (cl = 1) or the cl CTAs of a cluster, each of which is sent all warps'
 // partial sums.  Two generations of partial sums are used in turn, so one
-// barrier per sum is enough: a thread that runs ahead writes the other
-// generation, and cannot come back to this one before every thread has
-// passed the barrier in between.
+// wait per sum is enough: a thread that runs ahead writes the other
+// generation, and cannot come back to this one before it has the sum in
+// between, to which every warp contributes only after reading this one.
+// Within a cluster the values are counted by an mbarrier of the receiving
+// CTA: a barrier of the whole cluster would also wait for the row's stores
+// (measured at 16,384 rows of 8,192 columns: 487 us, against the time above
+// the plan in la2_api.cu).  A wait that gives up leaves a stale sum; the
+// caller's loop runs on, so that no barrier is missed, and the error word
+// tells the host.
 constexpr int kMaxCluster = 8;
 template <int TPR, int K>
 struct RowSum {
   static constexpr int NW = TPR / 32;
-  using Shared = float[2][K][TPR > 32 ? kMaxCluster * NW : 1];
-  int turn = 0;
-  __device__ __forceinline__ void operator()(float (&x)[K], Shared &red, int cl, int rank) {
+  struct Shared {
+    uint64_t bars[2];
+    float red[2][K][TPR > 32 ? kMaxCluster * NW : 1];
+  };
+  uint32_t uses = 0;
+  // before the first sum, by all threads; a barrier of the CTA (cl = 1: none
+  // is needed) and of the cluster follow
+  __device__ __forceinline__ void init(Shared &s, int cl) {
+    if (TPR > 32 && cl > 1 && threadIdx.x == 0) {
+      for (int g = 0; g < 2; g++) {
+        mbar_init(smem_u32(&s.bars[g]), 1);
+        fence_mbar_init();
+        mbar_expect_tx(smem_u32(&s.bars[g]), (uint32_t)(cl * NW * K * sizeof(float)));
+      }
+    }
+  }
+  __device__ __forceinline__ void operator()(float (&x)[K], Shared &s, int cl, int rank,
+                                             volatile int *abort) {
     lanes_sum<K, 32>(x);
     if constexpr (TPR > 32) {
-      const int w = threadIdx.x / 32, l = threadIdx.x % 32;
+      const int w = threadIdx.x / 32, l = threadIdx.x % 32, turn = uses & 1;
       if (cl == 1) {
         if (l == 0) {
 #pragma unroll
-          for (int k = 0; k < K; k++) red[turn][k][w] = x[k];
+          for (int k = 0; k < K; k++) s.red[turn][k][w] = x[k];
         }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < K; k++) x[k] = red[turn][k][l % NW];
+        for (int k = 0; k < K; k++) x[k] = s.red[turn][k][l % NW];
         lanes_sum<K, NW>(x);
       } else {
+        const uint32_t bar = smem_u32(&s.bars[turn]);
         if (l < cl) {
 #pragma unroll
-          for (int k = 0; k < K; k++) store_in_cta(&red[turn][k][rank * NW + w], l, x[k]);
+          for (int k = 0; k < K; k++) send(smem_u32(&s.red[turn][k][rank * NW + w]), bar, l, x[k]);
         }
-        cluster_arrive_wait();
+        mbar_wait(bar, (uses >> 1) & 1, abort);
+        if (threadIdx.x == 0) mbar_expect_tx(bar, (uint32_t)(cl * NW * K * sizeof(float)));
 #pragma unroll
         for (int k = 0; k < K; k++) {
           x[k] = 0.f;
-          for (int j = l; j < cl * NW; j += 32) x[k] += red[turn][k][j];
+          for (int j = l; j < cl * NW; j += 32) x[k] += s.red[turn][k][j];
         }
         lanes_sum<K, 32>(x);
       }
-      turn ^= 1;
+      uses++;
     }
   }
 };
@@ -359,7 +385,13 @@ gated_kernel(const __grid_constant__ Gated p) {
   const int c0 = (ROW ? rank : (int)blockIdx.y) * p.cols;
   const int end = c0 + p.cols < D ? c0 + p.cols : D;
   const float inv = 1.f / (float)(ROW ? D : e);
-  if (ROW && TPR > 32 && cl > 1) cluster_arrive_wait();  // every CTA's shared memory is there
+  __shared__ int abort;
+  if (ROW && TPR > 32 && cl > 1) {
+    if (threadIdx.x == 0) abort = 0;
+    row_sum.init(red, cl);
+    __syncthreads();
+    cluster_arrive_wait();  // every CTA's barriers are there
+  }
 
   int c[NV];
   int64_t at_o[NV];
@@ -514,7 +546,7 @@ gated_kernel(const __grid_constant__ Gated p) {
       for (int n = 1; n < NV; n++)
 #pragma unroll
         for (int k = 0; k < (GRAD ? 2 : 1); k++) sum[0][k] += sum[n][k];
-      row_sum(sum[0], red, cl, rank);
+      row_sum(sum[0], red, cl, rank, &abort);
 #pragma unroll
       for (int n = 1; n < NV; n++)
 #pragma unroll
@@ -568,6 +600,7 @@ gated_kernel(const __grid_constant__ Gated p) {
     }
     advance(to);
   }
+  if (ROW && TPR > 32 && cl > 1) cluster_arrive_wait();  // none leaves while another sends
   if constexpr (GRAD) {
     if (!p.dw) return;
     launch_dependents();
@@ -614,12 +647,13 @@ struct Residual {
 
 // Rows wider than a warp holds come through a ring of one or two rows in
 // shared memory, filled by thread 0 with one bulk copy per stream.  A row's
-// stage is given back by the block barrier of its first reduction, which no
-// thread passes before all have taken their values into registers; so even
+// stage is given back by the block barrier of its first reduction (in a
+// cluster, the one after it), which no thread passes before all have taken
+// their values into registers; so even
 // one stage is filled again while its last row is worked on.  The weights
 // stand in front of the ring: with two CTAs on an SM little is left of the
 // L1 cache, and read from L2 for every row they cost as much as a stream.
-constexpr int kRingHead = 128;  // barriers and the flag, in front of the ring
+constexpr int kRingHead = 128;  // barriers, in front of the ring
 
 __device__ __forceinline__ void bulk_row(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -658,7 +692,15 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
   const T *y = static_cast<const T *>(p.y);
   const int64_t step = (int64_t)(gridDim.x / cl) * RPC;
   const int64_t first = (int64_t)(blockIdx.x / cl) * RPC;
-  if (cl > 1) cluster_arrive_wait();  // every CTA's shared memory is there
+  __shared__ int gave_up;
+  volatile int *abort = &gave_up;
+  if constexpr (TPR > 32) {
+    if (threadIdx.x == 0) gave_up = 0;
+    sum.init(red, cl);
+    sum1.init(red1, cl);
+    __syncthreads();
+    if (cl > 1) cluster_arrive_wait();  // every CTA's barriers are there
+  }
 
   // unit n: its first column, and moves of its eight values
   auto col = [&](int n) { return ONE ? n * 8 * TPR + tr : (n * TPR + tr) * 8; };
@@ -692,7 +734,6 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
   const uint32_t hb = (uint32_t)width * sizeof(R), yb = (uint32_t)width * sizeof(T);
   const bool has_g = GRAD && p.dh_new, has_y = HAS_Y && y;
   const uint32_t bars = smem_u32(dyn);
-  volatile int *abort = reinterpret_cast<volatile int *>(dyn + 64);
   const uint32_t at_g = hb, at_s = at_g + (has_g ? hb : 0), at_y = at_s + (GRAD ? yb : 0);
   const uint32_t row_bytes = at_y + (has_y ? yb : 0), stage_bytes = (row_bytes + 127) / 128 * 128;
   char *ring = dyn + kRingHead + (POST ? 2 : 1) * sizeof(float) * p.cols;
@@ -709,7 +750,6 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
     if (threadIdx.x == 0) {
       mbar_init(bars, 1);
       mbar_init(bars + 8, 1);
-      *abort = 0;
       fence_mbar_init();
     }
     __syncthreads();
@@ -790,6 +830,7 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
     // after the row's first barrier: its stage is free
     auto refill = [&] {
       if constexpr (RING) {
+        if (cl > 1) __syncthreads();
         const int64_t later = r0 + p.stages * step;
         if (threadIdx.x == 0 && later < p.rows) fetch(later, st);
       }
@@ -811,7 +852,7 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
             for (int i = 0; i < P; i++) q2 = fma2(z[i], z[i], q2);
           }
           float q[1] = {q2.x + q2.y};
-          sum1(q, red1, cl, rank);
+          sum1(q, red1, cl, rank, abort);
           refill();
           refilled = true;
           ry = pair(rsqrtf(fmaf(q[0], inv, p.eps)) * p.beta);
@@ -838,7 +879,7 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
 #pragma unroll
         for (int i = 0; i < P; i++) q2 = fma2(x[n][i], x[n][i], q2);
       float q[1] = {q2.x + q2.y};
-      sum(q, red, cl, rank);
+      sum(q, red, cl, rank, abort);
       if (!refilled) refill();
       const float2 rstd = pair(rsqrtf(fmaf(q[0], inv, p.eps)));
 #pragma unroll
@@ -875,7 +916,7 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
         }
       }
       float q[3] = {q0.x + q0.y, q1.x + q1.y, q2.x + q2.y};
-      sum(q, red, cl, rank);
+      sum(q, red, cl, rank, abort);
       refill();
       const float r = rsqrtf(fmaf(q[0], inv, p.eps));
       const float2 rstd = pair(r), m = pair(-q[1] * r * inv);  // -mean(s hn)
@@ -917,7 +958,7 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
         float2 mz = pair(0.f);               // -mean((dp pw) yn) / rms(y)
         if constexpr (POST) {
           float t[1] = {k.x + k.y};
-          sum1(t, red1, cl, rank);
+          sum1(t, red1, cl, rank, abort);
           mz = mul2(pair(-t[0] * inv), ry);
         }
 #pragma unroll
@@ -935,6 +976,7 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
       }
     }
   }
+  if (cl > 1) cluster_arrive_wait();  // none leaves while another sends
   if constexpr (RING) {
     // after a timeout: let the rows in flight land before the ring is released
     if (threadIdx.x == 0 && *abort) {
