@@ -633,13 +633,14 @@ constexpr int kNormMaxCols = 16384;  // widest row that one CTA holds
 struct NormPlan {
   int nt, tpr, nv, cols, slices, cl, rpc;
 };
-// The row's width decides who holds it (see la2_norm.cuh): a warp, a CTA with
-// one or two vectors per thread, or a cluster of CTAs.  `one` values at a time
-// where no 16-byte piece divides the row.
+// The row's width decides who holds it (see la2_norm.cuh): a warp, a CTA of 128
+// or 256 threads with up to `most_units` units of eight values each, or a
+// cluster of CTAs.  one: values that lie apart, where no 16-byte piece divides
+// the row.
 NormPlan row_plan(int D, bool one, int most_units = 2) {
   NormPlan g;
   g.slices = 1;
-  const int most = one ? 2048 : 2048 * most_units;
+  const int most = 2048 * most_units;
   g.cl = 1;
   while (g.cl * most < D) g.cl *= 2;
   const int unit = one ? 1 : 8;
@@ -648,9 +649,12 @@ NormPlan row_plan(int D, bool one, int most_units = 2) {
     g.nt = 128;
     g.tpr = 32;
     g.nv = 2;
+  } else if (!one && D <= 1024) {
+    g.nt = g.tpr = 128;
+    g.nv = 1;
   } else {
     g.nt = g.tpr = 256;
-    g.nv = one || g.cols <= 2048 ? 1 : g.cols <= 4096 ? 2 : 4;
+    g.nv = g.cols <= 2048 ? 1 : g.cols <= 4096 ? 2 : 4;
   }
   g.rpc = g.nt / g.tpr;
   return g;
@@ -761,6 +765,7 @@ cudaError_t gated_shape(const la2::norm::Gated &p, bool row, float *dw, cudaStre
   }
   const NormPlan g = row_plan(p.H * p.e, false);
   if (g.tpr == 32) return gated_launch<T, 0, true, GRAD, GATE, 128, 32, 2>(p, g, dw, st);
+  if (g.tpr == 128) return gated_launch<T, 0, true, GRAD, GATE, 128, 128, 1>(p, g, dw, st);
   if (g.nv == 1) return gated_launch<T, 0, true, GRAD, GATE, 256, 256, 1>(p, g, dw, st);
   return gated_launch<T, 0, true, GRAD, GATE, 256, 256, 2>(p, g, dw, st);
 }
@@ -779,22 +784,31 @@ cudaError_t gated_call(const la2::norm::Gated &p, la2_dtype dt, unsigned flags, 
                        : gated_gate<__nv_bfloat16, GRAD>(p, flags, dw, st);
 }
 
+// What two residual norm's CTAs on an SM may each have: half of its shared
+// memory less what the system and the kernel's static arrays take.
+constexpr size_t two_ctas(bool grad) { return 233472 / 2 - 1024 - (grad ? 1200 : 640); }
+// Shared memory of such a CTA: the weights and `stages` rows of the streams
+// that there are.
+template <typename T, typename R, bool POST, bool GRAD, bool ONE>
+size_t residual_smem(const la2::norm::Residual &p, int cols, int stages) {
+  using la2::norm::row_room;
+  size_t row = row_room<R, ONE>(cols);
+  if (GRAD) row += (p.dh_new ? row_room<R, ONE>(cols) : 0) + row_room<T, ONE>(cols);
+  if (GRAD ? POST : p.y != nullptr) row += row_room<T, ONE>(cols);
+  return la2::norm::kRingHead + (size_t)((cols + 3) / 4 * 4) * sizeof(float) * (POST ? 2 : 1) +
+         stages * row;
+}
+
 template <typename T, typename R, bool POST, bool GRAD, bool ONE, int NT, int TPR, int NV>
 cudaError_t residual_launch(la2::norm::Residual p, const NormPlan &g, float *dw, float *dpw,
                             cudaStream_t st) {
   auto kern = la2::norm::residual_kernel<T, R, GRAD, POST, ONE, NT, TPR, NV>;
   size_t smem = 0;
-  if (!ONE && TPR > 32) {
-    // the weights, and two rows of every stream where two CTAs on an SM have
-    // room for them, else one
-    size_t row = (size_t)g.cols * sizeof(R);
-    if (GRAD) row += (p.dh_new ? (size_t)g.cols * sizeof(R) : 0) + (size_t)g.cols * sizeof(T);
-    if (GRAD ? POST : p.y != nullptr) row += (size_t)g.cols * sizeof(T);
-    row = (row + 127) / 128 * 128;
-    const size_t head = la2::norm::kRingHead + (size_t)g.cols * sizeof(float) * (POST ? 2 : 1);
-    p.stages = head + 2 * row <= 112 * 1024 ? 2 : 1;
-    smem = head + p.stages * row;
-  } else if (GRAD && TPR == 32) {
+  if (TPR > 32) {
+    // two rows where two CTAs on an SM have room for them, else one
+    p.stages = residual_smem<T, R, POST, GRAD, ONE>(p, g.cols, 2) <= two_ctas(GRAD) ? 2 : 1;
+    smem = residual_smem<T, R, POST, GRAD, ONE>(p, g.cols, p.stages);
+  } else if (GRAD) {
     smem = (size_t)NT * NV * 8 * sizeof(float);
   }
   if (smem > 32 * 1024)  // 48 KB with the static arrays go without
@@ -815,10 +829,17 @@ cudaError_t residual_launch(la2::norm::Residual p, const NormPlan &g, float *dw,
 
 template <typename T, typename R, bool POST, bool GRAD>
 cudaError_t residual_shape(const la2::norm::Residual &p, float *dw, float *dpw, cudaStream_t st) {
-  const bool one = p.D % 8 != 0;
-  const NormPlan g = row_plan(p.D, one, GRAD ? 2 : 4);
-  if (one) return residual_launch<T, R, POST, GRAD, true, 256, 256, 1>(p, g, dw, dpw, st);
+  if (p.D % 8 != 0) {
+    const NormPlan g = row_plan(p.D, true);
+    return g.nv == 1 ? residual_launch<T, R, POST, GRAD, true, 256, 256, 1>(p, g, dw, dpw, st)
+                     : residual_launch<T, R, POST, GRAD, true, 256, 256, 2>(p, g, dw, dpw, st);
+  }
+  NormPlan g = row_plan(p.D, false, GRAD ? 2 : 4);
+  // 8,192 columns in a CTA only where two such CTAs fit an SM
+  if (g.nv == 4 && residual_smem<T, R, POST, GRAD, false>(p, g.cols, 1) > two_ctas(GRAD))
+    g = row_plan(p.D, false, 2);
   if (g.tpr == 32) return residual_launch<T, R, POST, GRAD, false, 128, 32, 2>(p, g, dw, dpw, st);
+  if (g.tpr == 128) return residual_launch<T, R, POST, GRAD, false, 128, 128, 1>(p, g, dw, dpw, st);
   if (g.nv == 1) return residual_launch<T, R, POST, GRAD, false, 256, 256, 1>(p, g, dw, dpw, st);
   if constexpr (!GRAD)
     if (g.nv == 4) return residual_launch<T, R, POST, GRAD, false, 256, 256, 4>(p, g, dw, dpw, st);

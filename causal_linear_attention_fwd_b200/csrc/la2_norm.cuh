@@ -29,10 +29,10 @@
 // own next values into shared memory, the residual norm (contiguous rows)
 // takes them by bulk copies into a ring of rows there.
 //
-// A row is held by a warp (up to 512 columns), a CTA (up to 4,096; 2,048 where
-// values move one by one) or a cluster of 2 to 8 CTAs that add their partial
-// sums through distributed shared memory: a thread's share, and so the
-// registers it takes, stays the same at every width.
+// A row is held by a warp (up to 512 columns), a CTA (up to 4,096, or 8,192 in
+// the residual norm's forward) or a cluster of 2 or 4 CTAs that add their
+// partial sums through distributed shared memory: a thread's share, and so
+// the registers it takes, stays bounded at every width.
 //
 // The weights' gradients are column sums over all rows.  A thread keeps its
 // columns over all rows its CTA walks, so each CTA (or cluster) writes one row
@@ -164,10 +164,11 @@ __device__ __forceinline__ void weights8(const float *w, float2 (&f)[4]) {
     f[3] = make_float2(y.z, y.w);
   }
 }
+// the same of strided values in shared memory
 __device__ __forceinline__ void weights_strided(const float *w, float2 (&f)[4], int stride, int left) {
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    const float x = !w ? 1.f : i * stride < left ? __ldg(w + i * stride) : 0.f;
+    const float x = i * stride < left ? w[i * stride] : 0.f;
     if (i % 2) f[i / 2].y = x;
     else f[i / 2].x = x;
   }
@@ -253,7 +254,7 @@ __device__ __forceinline__ void send(uint32_t to, uint32_t bar, uint32_t rank, f
 // the plan in la2_api.cu).  A wait that gives up leaves a stale sum; the
 // caller's loop runs on, so that no barrier is missed, and the error word
 // tells the host.
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 4;
 template <int TPR, int K>
 struct RowSum {
   static constexpr int NW = TPR / 32;
@@ -670,11 +671,17 @@ struct RowData {
   Raw<T> s[GRAD ? NV : 1], y[(GRAD && !POST) ? 1 : NV];
 };
 
+// Bytes of a stage for one stream.
+template <typename T, bool ONE>
+__host__ __device__ constexpr uint32_t row_room(int cols) {
+  return (uint32_t)(cols * sizeof(T) + (ONE ? 30 : 0) + 15) / 16 * 16;
+}
+
 // ONE: rows that no 16-byte piece divides (units of strided values).  TPR
 // threads hold a row, NV units of eight values each.
 template <typename T, typename R, bool GRAD, bool POST, bool ONE, int NT, int TPR, int NV>
 __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__ Residual p) {
-  constexpr bool RING = !ONE && TPR > 32;
+  constexpr bool RING = TPR > 32;
   constexpr bool HAS_Y = !GRAD || POST;  // y may be read
   constexpr int RPC = NT / TPR, P = 4;
   using Sum = RowSum<TPR, GRAD ? 3 : 1>;
@@ -704,20 +711,22 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
 
   // unit n: its first column, and moves of its eight values
   auto col = [&](int n) { return ONE ? n * 8 * TPR + tr : (n * TPR + tr) * 8; };
-  auto get = [&](auto &raw, const auto *row, int c) {
+  auto get_shared = [&](auto &raw, const auto *row, int c) {
     if constexpr (ONE) raw.load_strided(row + c, TPR, width - c);
-    else raw.load(row + c);
+    else raw.load_shared(row + c);
   };
   auto put = [&](auto *row, int c, const float2 (&x)[P]) {
     if constexpr (ONE) store_strided(row + c, x, TPR, width - c);
     else store_pairs(row + c, x);
   };
   // weights (0: w, 1: pw) of a unit.  In shared memory the first and the last
-  // four of each unit lie apart, so that a warp reads whole lines.
+  // four of a unit of neighbours lie apart, so that a warp reads whole lines.
   float4 *held = reinterpret_cast<float4 *>(dyn + kRingHead);
-  const int units = p.cols / 8;
+  const int units = p.cols / 8, room = (p.cols + 3) / 4 * 4;
   auto weights = [&](int which, int c, float2 (&x)[P]) {
-    if constexpr (RING) {
+    if constexpr (RING && ONE) {
+      weights_strided(reinterpret_cast<float *>(held) + which * room + c, x, TPR, width - c);
+    } else if constexpr (RING) {
       const float4 a = held[2 * which * units + c / 8], b = held[(2 * which + 1) * units + c / 8];
       x[0] = make_float2(a.x, a.y);
       x[1] = make_float2(a.z, a.w);
@@ -725,26 +734,53 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
       x[3] = make_float2(b.z, b.w);
     } else {
       const float *w = which ? p.post_weight : p.weight;
-      if constexpr (ONE) weights_strided(w ? w + c0 + c : w, x, TPR, width - c);
-      else weights8(w ? w + c0 + c : w, x);
+      weights8(w ? w + c : w, x);
     }
   };
 
-  // a stage of the ring: h | dh' | dn | y, the ones that are
-  const uint32_t hb = (uint32_t)width * sizeof(R), yb = (uint32_t)width * sizeof(T);
+  // A stage of the ring: h | dh' | dn | y, the ones that are.  A bulk copy
+  // moves whole 16-byte pieces: where rows (ONE) begin or end inside one, the
+  // pieces around the row are copied and it is read from `lead` bytes on; the
+  // last pieces of the whole tensor, of which bytes lie behind its end, come
+  // value by value.
+  const int64_t total = p.rows * p.D;
   const bool has_g = GRAD && p.dh_new, has_y = HAS_Y && y;
   const uint32_t bars = smem_u32(dyn);
+  const uint32_t hb = row_room<R, ONE>(p.cols), yb = row_room<T, ONE>(p.cols);
   const uint32_t at_g = hb, at_s = at_g + (has_g ? hb : 0), at_y = at_s + (GRAD ? yb : 0);
-  const uint32_t row_bytes = at_y + (has_y ? yb : 0), stage_bytes = (row_bytes + 127) / 128 * 128;
-  char *ring = dyn + kRingHead + (POST ? 2 : 1) * sizeof(float) * p.cols;
+  const uint32_t stage_bytes = at_y + (has_y ? yb : 0);
+  char *ring = dyn + kRingHead + (POST ? 2 : 1) * sizeof(float) * room;
+  auto lead = [&](int64_t at, int es) { return ONE ? (uint32_t)(at * es) & 15u : 0u; };
+  auto fetch_one = [&](const auto *x, int64_t at, char *to, uint32_t bar) -> uint32_t {
+    using X = typename std::remove_const<typename std::remove_pointer<decltype(x)>::type>::type;
+    constexpr int es = sizeof(X);
+    if constexpr (!ONE) {
+      bulk_row(smem_u32(to), x + at, (uint32_t)width * es, bar);
+      return 0;
+    } else {
+      const char *from = reinterpret_cast<const char *>(x + at) - lead(at, es);
+      uint32_t bytes = (lead(at, es) + (uint32_t)width * es + 15u) / 16u * 16u;
+      if (from + bytes > reinterpret_cast<const char *>(x + total)) {
+        bytes -= 16;
+        const int first = ((int)bytes - (int)lead(at, es)) / es;  // the first column not copied
+        X *s = reinterpret_cast<X *>(to + bytes);
+        for (int i = first < 0 ? -first : 0; first + i < width; i++) s[i] = x[at + first + i];
+      }
+      if (bytes) bulk_row(smem_u32(to), from, bytes, bar);
+      return bytes;
+    }
+  };
   auto fetch = [&](int64_t row, int st) {  // thread 0
-    const uint32_t bar = bars + st * 8, dst = smem_u32(ring) + st * stage_bytes;
+    const uint32_t bar = bars + st * 8;
+    char *to = ring + st * stage_bytes;
     const int64_t at = row * p.D + c0;
-    mbar_expect_tx(bar, row_bytes);
-    bulk_row(dst, static_cast<const R *>(p.h) + at, hb, bar);
-    if (has_g) bulk_row(dst + at_g, static_cast<const R *>(p.dh_new) + at, hb, bar);
-    if (GRAD) bulk_row(dst + at_s, static_cast<const T *>(p.dn) + at, yb, bar);
-    if (has_y) bulk_row(dst + at_y, y + at, yb, bar);
+    if constexpr (!ONE)
+      mbar_expect_tx(bar, (uint32_t)width * ((has_g ? 2 : 1) * sizeof(R) + (GRAD + has_y) * sizeof(T)));
+    uint32_t bytes = fetch_one(static_cast<const R *>(p.h), at, to, bar);
+    if (has_g) bytes += fetch_one(static_cast<const R *>(p.dh_new), at, to + at_g, bar);
+    if (GRAD) bytes += fetch_one(static_cast<const T *>(p.dn), at, to + at_s, bar);
+    if (has_y) bytes += fetch_one(y, at, to + at_y, bar);
+    if constexpr (ONE) mbar_expect_tx(bar, bytes);
   };
   if constexpr (RING) {
     if (threadIdx.x == 0) {
@@ -757,7 +793,12 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
       if (first < p.rows) fetch(first, 0);
       if (p.stages > 1 && first + step < p.rows) fetch(first + step, 1);
     }
-    for (int i = threadIdx.x; i < (POST ? 2 : 1) * units; i += NT) {
+    for (int i = threadIdx.x; ONE && i < (POST ? 2 : 1) * room; i += NT) {
+      const int which = i >= room, c = i - which * room;
+      const float *w = which ? p.post_weight : p.weight;
+      reinterpret_cast<float *>(held)[i] = w && c < width ? __ldg(w + c0 + c) : 1.f;
+    }
+    for (int i = threadIdx.x; !ONE && i < (POST ? 2 : 1) * units; i += NT) {
       const int which = i >= units, u = i - which * units;
       const float *w = which ? p.post_weight : p.weight;
       if (u * 8 < width) {
@@ -798,24 +839,25 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
       const int c = col(n);
       if (live && c < width) {
         if constexpr (RING) {
-          d.h[n].load_shared(reinterpret_cast<const R *>(stage) + c);
+          const char *hr = stage + lead(at, sizeof(R)), *yr = stage + lead(at, sizeof(T));
+          get_shared(d.h[n], reinterpret_cast<const R *>(hr), c);
           if constexpr (GRAD) {
-            if (has_g) d.g[n].load_shared(reinterpret_cast<const R *>(stage + at_g) + c);
+            if (has_g) get_shared(d.g[n], reinterpret_cast<const R *>(hr + at_g), c);
             else d.g[n].clear();
-            d.s[n].load_shared(reinterpret_cast<const T *>(stage + at_s) + c);
+            get_shared(d.s[n], reinterpret_cast<const T *>(yr + at_s), c);
           }
           if constexpr (HAS_Y) {
-            if (has_y) d.y[n].load_shared(reinterpret_cast<const T *>(stage + at_y) + c);
+            if (has_y) get_shared(d.y[n], reinterpret_cast<const T *>(yr + at_y), c);
           }
         } else {
-          get(d.h[n], static_cast<const R *>(p.h) + at, c);
+          d.h[n].load(static_cast<const R *>(p.h) + at + c);
           if constexpr (GRAD) {
-            if (has_g) get(d.g[n], static_cast<const R *>(p.dh_new) + at, c);
+            if (has_g) d.g[n].load(static_cast<const R *>(p.dh_new) + at + c);
             else d.g[n].clear();
-            get(d.s[n], static_cast<const T *>(p.dn) + at, c);
+            d.s[n].load(static_cast<const T *>(p.dn) + at + c);
           }
           if constexpr (HAS_Y) {
-            if (has_y) get(d.y[n], y + at, c);
+            if (has_y) d.y[n].load(y + at + c);
           }
         }
       } else {
