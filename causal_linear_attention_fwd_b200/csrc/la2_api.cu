@@ -632,24 +632,25 @@ constexpr int kNormMaxCols = 16384;  // widest row that one CTA holds
 // How a norm's CTAs cover rows and columns.
 struct NormPlan {
   int nt, tpr, nv, cols, slices, cl, rpc;
+  bool odd;
 };
 // The row's width decides who holds it (see la2_norm.cuh): a warp, a CTA of 128
 // or 256 threads with up to `most_units` units of eight values each, or a
-// cluster of CTAs.  one: values that lie apart, where no 16-byte piece divides
-// the row.
-NormPlan row_plan(int D, bool one, int most_units = 2) {
+// cluster of CTAs.  odd: rows that begin anywhere between two 16-byte pieces
+// (up to 7 places more).
+NormPlan row_plan(int D, bool odd, int most_units = 2) {
   NormPlan g;
   g.slices = 1;
-  const int most = 2048 * most_units;
+  g.odd = odd;
+  const int places = odd ? D + 7 : D, most = 2048 * most_units;
   g.cl = 1;
-  while (g.cl * most < D) g.cl *= 2;
-  const int unit = one ? 1 : 8;
-  g.cols = ((D + unit - 1) / unit + g.cl - 1) / g.cl * unit;
-  if (!one && D <= 512) {
+  while (g.cl * most < places) g.cl *= 2;
+  g.cols = ((places + 7) / 8 + g.cl - 1) / g.cl * 8;
+  if (places <= 512) {
     g.nt = 128;
     g.tpr = 32;
     g.nv = 2;
-  } else if (!one && D <= 1024) {
+  } else if (!odd && places <= 1024) {
     g.nt = g.tpr = 128;
     g.nv = 1;
   } else {
@@ -662,6 +663,7 @@ NormPlan row_plan(int D, bool one, int most_units = 2) {
 // Per head: the most heads side by side that divide H, so no lane is idle.
 NormPlan head_plan(int H, int e) {
   NormPlan g;
+  g.odd = false;
   g.nt = 256;
   g.nv = 1;
   g.cl = 1;
@@ -673,18 +675,24 @@ NormPlan head_plan(int H, int e) {
   g.rpc = g.nt / g.tpr;
   return g;
 }
-// Groups of CTAs (one row of partial sums each) that walk the rows.
+// Groups of CTAs (one row of partial sums each) that walk the rows.  Odd rows:
+// where a group walks more than one, they lie a multiple of 8 apart.
 int64_t norm_groups(int64_t rows, const NormPlan &g, int per_sm) {
   const int64_t need = (rows + g.rpc - 1) / g.rpc;
   const int64_t full = (int64_t)device_sms() * per_sm / (g.slices * g.cl);
-  return need < full ? need : (full > 1 ? full : 1);
+  if (need <= full) return need;
+  if (g.odd) return full > 8 ? full / 8 * 8 : 8;
+  return full > 1 ? full : 1;
 }
+
+// Floats of one weight's partial sums, so that another's begin aligned.
+size_t partial_floats(int64_t groups, int D) { return ((size_t)groups * D + 7) / 8 * 8; }
 
 size_t norm_ws_bytes(int op, int B, int H, int64_t L, int d, int e, la2_dtype dt) {
   if (!dtype_ok(dt)) return 0;
   if (op == LA2_OP_RESIDUAL_NORM_BACKWARD) {
     if (d < 1 || d > kNormMaxCols) return 0;
-    return (size_t)norm_groups((int64_t)B * H * L, row_plan(d, d % 8 != 0), kNormGradPerSm) * d *
+    return partial_floats(norm_groups((int64_t)B * H * L, row_plan(d, d % 8 != 0), kNormGradPerSm), d) *
            sizeof(float) * 2;
   }
   if (e != 64 && e != 128) return 0;
@@ -786,30 +794,31 @@ cudaError_t gated_call(const la2::norm::Gated &p, la2_dtype dt, unsigned flags, 
 
 // What two residual norm's CTAs on an SM may each have: half of its shared
 // memory less what the system and the kernel's static arrays take.
-constexpr size_t two_ctas(bool grad) { return 233472 / 2 - 1024 - (grad ? 1200 : 640); }
+constexpr size_t two_ctas(bool grad, bool odd) {
+  return 233472 / 2 - 1024 - (grad ? 1200 : 640) * (odd ? 2 : 1);
+}
 // Shared memory of such a CTA: the weights and `stages` rows of the streams
 // that there are.
-template <typename T, typename R, bool POST, bool GRAD, bool ONE>
+template <typename T, typename R, bool POST, bool GRAD>
 size_t residual_smem(const la2::norm::Residual &p, int cols, int stages) {
-  using la2::norm::row_room;
-  size_t row = row_room<R, ONE>(cols);
-  if (GRAD) row += (p.dh_new ? row_room<R, ONE>(cols) : 0) + row_room<T, ONE>(cols);
-  if (GRAD ? POST : p.y != nullptr) row += row_room<T, ONE>(cols);
-  return la2::norm::kRingHead + (size_t)((cols + 3) / 4 * 4) * sizeof(float) * (POST ? 2 : 1) +
-         stages * row;
+  size_t row = sizeof(R);
+  if (GRAD) row += (p.dh_new ? sizeof(R) : 0) + sizeof(T);
+  if (GRAD ? POST : p.y != nullptr) row += sizeof(T);
+  return la2::norm::kRingHead + (size_t)cols * (sizeof(float) * (POST ? 2 : 1) + stages * row);
 }
 
-template <typename T, typename R, bool POST, bool GRAD, bool ONE, int NT, int TPR, int NV>
+template <typename T, typename R, bool POST, bool GRAD, bool ODD, int NT, int TPR, int NV>
 cudaError_t residual_launch(la2::norm::Residual p, const NormPlan &g, float *dw, float *dpw,
                             cudaStream_t st) {
-  auto kern = la2::norm::residual_kernel<T, R, GRAD, POST, ONE, NT, TPR, NV>;
+  auto kern = la2::norm::residual_kernel<T, R, GRAD, POST, ODD, NT, TPR, NV>;
   size_t smem = 0;
+  p.stages = 1;
   if (TPR > 32) {
     // two rows where two CTAs on an SM have room for them, else one
-    p.stages = residual_smem<T, R, POST, GRAD, ONE>(p, g.cols, 2) <= two_ctas(GRAD) ? 2 : 1;
-    smem = residual_smem<T, R, POST, GRAD, ONE>(p, g.cols, p.stages);
+    p.stages = residual_smem<T, R, POST, GRAD>(p, g.cols, 2) <= two_ctas(GRAD, ODD) ? 2 : 1;
+    smem = residual_smem<T, R, POST, GRAD>(p, g.cols, p.stages);
   } else if (GRAD) {
-    smem = (size_t)NT * NV * 8 * sizeof(float);
+    smem = (size_t)(NT / TPR) * p.D * sizeof(float);
   }
   if (smem > 32 * 1024)  // 48 KB with the static arrays go without
     if (cudaError_t e = opt_in_smem(kern, smem)) return e;
@@ -819,7 +828,7 @@ cudaError_t residual_launch(la2::norm::Residual p, const NormPlan &g, float *dw,
   const int64_t groups = norm_groups(p.rows, g, per_sm);
   p.cols = g.cols;
   p.cl = g.cl;
-  if (GRAD && dpw) p.dpw = p.dw + groups * p.D;
+  if (GRAD && dpw) p.dpw = p.dw + partial_floats(groups, p.D);
   if (!dw) p.dw = nullptr;
   cudaError_t e = timed(GRAD ? K_RESIDUAL_NORM_GRAD : K_RESIDUAL_NORM, st,
                         [&] { return launch_groups(kern, p, g, groups, smem, st); });
@@ -831,12 +840,13 @@ template <typename T, typename R, bool POST, bool GRAD>
 cudaError_t residual_shape(const la2::norm::Residual &p, float *dw, float *dpw, cudaStream_t st) {
   if (p.D % 8 != 0) {
     const NormPlan g = row_plan(p.D, true);
-    return g.nv == 1 ? residual_launch<T, R, POST, GRAD, true, 256, 256, 1>(p, g, dw, dpw, st)
-                     : residual_launch<T, R, POST, GRAD, true, 256, 256, 2>(p, g, dw, dpw, st);
+    if (g.tpr == 32) return residual_launch<T, R, POST, GRAD, true, 128, 32, 2>(p, g, dw, dpw, st);
+    if (g.nv == 1) return residual_launch<T, R, POST, GRAD, true, 256, 256, 1>(p, g, dw, dpw, st);
+    return residual_launch<T, R, POST, GRAD, true, 256, 256, 2>(p, g, dw, dpw, st);
   }
   NormPlan g = row_plan(p.D, false, GRAD ? 2 : 4);
   // 8,192 columns in a CTA only where two such CTAs fit an SM
-  if (g.nv == 4 && residual_smem<T, R, POST, GRAD, false>(p, g.cols, 1) > two_ctas(GRAD))
+  if (g.nv == 4 && residual_smem<T, R, POST, GRAD>(p, g.cols, 1) > two_ctas(GRAD, false))
     g = row_plan(p.D, false, 2);
   if (g.tpr == 32) return residual_launch<T, R, POST, GRAD, false, 128, 32, 2>(p, g, dw, dpw, st);
   if (g.tpr == 128) return residual_launch<T, R, POST, GRAD, false, 128, 128, 1>(p, g, dw, dpw, st);

@@ -30,7 +30,7 @@
 // takes them by bulk copies into a ring of rows there.
 //
 // A row is held by a warp (up to 512 columns), a CTA (up to 4,096, or 8,192 in
-// the residual norm's forward) or a cluster of 2 or 4 CTAs that add their
+// the residual norm's forward) or a cluster of 2 to 8 CTAs that add their
 // partial sums through distributed shared memory: a thread's share, and so
 // the registers it takes, stays bounded at every width.
 //
@@ -52,11 +52,8 @@ namespace norm {
 using namespace sm100;
 
 // ------------------------------------------------------------ eight values
-// What a thread holds of a row: units of eight values as four pairs, so that
-// most arithmetic is done two at a time (mul2, fma2).  They are eight
-// neighbours moved as 16-byte pieces, or, in rows that no such piece divides,
-// eight values `stride` columns apart (neighbouring threads hold neighbouring
-// columns, so the loads of a warp stay whole).
+// What a thread holds of a row: units of eight neighbours, moved as 16-byte
+// pieces and worked on as four pairs (mul2, fma2).
 template <typename T> struct Raw {
   static constexpr int N = 8 * sizeof(T) / 16;
   uint4 r[N];
@@ -72,13 +69,14 @@ template <typename T> struct Raw {
 #pragma unroll
     for (int i = 0; i < N; i++) r[i] = reinterpret_cast<const uint4 *>(p)[i];
   }
-  // values `stride` apart, zeros from the `left`-th column on
-  __device__ __forceinline__ void load_strided(const T *p, int stride, int left) {
+  // values lo <= i < hi alone, from an address with the element's alignment;
+  // the others are 0
+  __device__ __forceinline__ void load_some(const T *p, int lo, int hi) {
     using W = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
     const W *q = reinterpret_cast<const W *>(p);
     uint32_t v[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = i * stride < left ? q[i * stride] : 0u;
+    for (int i = 0; i < 8; i++) v[i] = i >= lo && i < hi ? q[i] : 0u;
     if constexpr (sizeof(T) == 4) {
       r[0] = make_uint4(v[0], v[1], v[2], v[3]);
       r[N - 1] = make_uint4(v[4], v[5], v[6], v[7]);
@@ -86,10 +84,25 @@ template <typename T> struct Raw {
       r[0] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
   }
-  // neighbours at an address with the element's alignment only
-  __device__ __forceinline__ void load_any(const T *p, bool vec) {
-    if (vec) load(p);
-    else load_strided(p, 1, 8);
+  // all but the values lo <= i < hi set to 0
+  __device__ __forceinline__ void keep(int lo, int hi) {
+    uint32_t m[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) m[i] = i >= lo && i < hi ? 0xffffffffu : 0u;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < N; i++) {
+        r[i].x &= m[4 * i];
+        r[i].y &= m[4 * i + 1];
+        r[i].z &= m[4 * i + 2];
+        r[i].w &= m[4 * i + 3];
+      }
+    } else {
+      r[0].x &= (m[0] & 0xffffu) | m[1] << 16;
+      r[0].y &= (m[2] & 0xffffu) | m[3] << 16;
+      r[0].z &= (m[4] & 0xffffu) | m[5] << 16;
+      r[0].w &= (m[6] & 0xffffu) | m[7] << 16;
+    }
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     constexpr int M = 8 / N;
@@ -120,11 +133,12 @@ __device__ __forceinline__ void store8(T *p, const float (&f)[8]) {
     fmap::st_stream(p + i * N, fmap::vec16<T>::pack(g));
   }
 }
+// the values lo <= i < hi alone
 template <typename T>
-__device__ __forceinline__ void store_strided(T *p, const float2 (&x)[4], int stride, int left) {
+__device__ __forceinline__ void store_some(T *p, const float2 (&x)[4], int lo, int hi) {
 #pragma unroll
   for (int i = 0; i < 8; i++)
-    if (i * stride < left) io<T>::st(p + i * stride, i % 2 ? x[i / 2].y : x[i / 2].x);
+    if (i >= lo && i < hi) io<T>::st(p + i, i % 2 ? x[i / 2].y : x[i / 2].x);
 }
 template <typename T>
 __device__ __forceinline__ void store_pairs(T *p, const float2 (&x)[4]) {
@@ -140,7 +154,7 @@ __device__ __forceinline__ void store_pairs(T *p, const float2 (&x)[4]) {
 template <typename T>
 __device__ __forceinline__ void store_any(T *p, const float2 (&x)[4], bool vec) {
   if (vec) store_pairs(p, x);
-  else store_strided(p, x, 1, 8);
+  else store_some(p, x, 0, 8);
 }
 // 16 bytes into shared memory, behind the thread's back.
 __device__ __forceinline__ void copy16_async(void *to, const void *from) {
@@ -164,11 +178,11 @@ __device__ __forceinline__ void weights8(const float *w, float2 (&f)[4]) {
     f[3] = make_float2(y.z, y.w);
   }
 }
-// the same of strided values in shared memory
-__device__ __forceinline__ void weights_strided(const float *w, float2 (&f)[4], int stride, int left) {
+// the weights lo <= i < hi alone (the others 0), at any alignment
+__device__ __forceinline__ void weights_some(const float *w, float2 (&f)[4], int lo, int hi) {
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    const float x = i * stride < left ? w[i * stride] : 0.f;
+    const float x = i >= lo && i < hi ? (w ? __ldg(w + i) : 1.f) : 0.f;
     if (i % 2) f[i / 2].y = x;
     else f[i / 2].x = x;
   }
@@ -254,13 +268,12 @@ __device__ __forceinline__ void send(uint32_t to, uint32_t bar, uint32_t rank, f
 // the plan in la2_api.cu).  A wait that gives up leaves a stale sum; the
 // caller's loop runs on, so that no barrier is missed, and the error word
 // tells the host.
-constexpr int kMaxCluster = 4;
-template <int TPR, int K>
+template <int TPR, int K, int MAXCL>
 struct RowSum {
   static constexpr int NW = TPR / 32;
   struct Shared {
     uint64_t bars[2];
-    float red[2][K][TPR > 32 ? kMaxCluster * NW : 1];
+    float red[2][K][TPR > 32 ? MAXCL * NW : 1];
   };
   uint32_t uses = 0;
   // before the first sum, by all threads; a barrier of the CTA (cl = 1: none
@@ -373,7 +386,7 @@ gated_kernel(const __grid_constant__ Gated p) {
   constexpr int V = 8, P = V / 2, LPH = ROW ? 32 : E / V;
   constexpr int S = gated_stages<T, NV>();
   constexpr bool HOLD = !(GRAD && NV == 2);  // the weights, in registers throughout
-  using Sum = RowSum<ROW ? TPR : 32, GRAD ? 2 : 1>;
+  using Sum = RowSum<ROW ? TPR : 32, GRAD ? 2 : 1, 4>;
   __shared__ typename Sum::Shared red;
   extern __shared__ __align__(128) char dyn[];
   Sum row_sum;
@@ -491,7 +504,7 @@ gated_kernel(const __grid_constant__ Gated p) {
             if (gate_ahead) cur.g[n].r[i] = *slot(stage, STREAMS - 1, n, i);
         }
         if constexpr (GATE != GATE_NONE)
-          if (!gate_ahead) cur.g[n].load_any(static_cast<const T *>(p.gate) + a.g + c[n], false);
+          if (!gate_ahead) cur.g[n].load_some(static_cast<const T *>(p.gate) + a.g + c[n], 0, 8);
       } else {
         cur.x[n].clear();
         if constexpr (GATE != GATE_NONE) cur.g[n].clear();
@@ -650,10 +663,18 @@ struct Residual {
 // shared memory, filled by thread 0 with one bulk copy per stream.  A row's
 // stage is given back by the block barrier of its first reduction (in a
 // cluster, the one after it), which no thread passes before all have taken
-// their values into registers; so even
-// one stage is filled again while its last row is worked on.  The weights
-// stand in front of the ring: with two CTAs on an SM little is left of the
-// L1 cache, and read from L2 for every row they cost as much as a stream.
+// their values into registers; so even one stage is filled again while its
+// last row is worked on.  The weights stand in front of the ring: with two
+// CTAs on an SM little is left of the L1 cache, and read from L2 for every row
+// they cost as much as a stream.
+//
+// ODD rows (D not a multiple of 8) begin anywhere between two 16-byte pieces.
+// Their units are laid from the piece that a row begins in, so that all but
+// the first and the last still move whole: a unit's values stand `lead`
+// places before its columns, lead = (row D) mod 8, and values before the row
+// or behind it are masked.  The host lets a thread's rows lie a multiple of 8
+// apart, so its lead, and with it its columns, its weights and its partial
+// sums, stay the same.
 constexpr int kRingHead = 128;  // barriers, in front of the ring
 
 __device__ __forceinline__ void bulk_row(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -671,21 +692,15 @@ struct RowData {
   Raw<T> s[GRAD ? NV : 1], y[(GRAD && !POST) ? 1 : NV];
 };
 
-// Bytes of a stage for one stream.
-template <typename T, bool ONE>
-__host__ __device__ constexpr uint32_t row_room(int cols) {
-  return (uint32_t)(cols * sizeof(T) + (ONE ? 30 : 0) + 15) / 16 * 16;
-}
-
-// ONE: rows that no 16-byte piece divides (units of strided values).  TPR
-// threads hold a row, NV units of eight values each.
-template <typename T, typename R, bool GRAD, bool POST, bool ONE, int NT, int TPR, int NV>
+// TPR threads hold a row, NV units each.
+template <typename T, typename R, bool GRAD, bool POST, bool ODD, int NT, int TPR, int NV>
 __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__ Residual p) {
   constexpr bool RING = TPR > 32;
   constexpr bool HAS_Y = !GRAD || POST;  // y may be read
   constexpr int RPC = NT / TPR, P = 4;
-  using Sum = RowSum<TPR, GRAD ? 3 : 1>;
-  using Sum1 = RowSum<TPR, 1>;
+  // 16,384 columns take four CTAs, the up to 7 places more of odd rows eight
+  using Sum = RowSum<TPR, GRAD ? 3 : 1, ODD ? 8 : 4>;
+  using Sum1 = RowSum<TPR, 1, ODD ? 8 : 4>;
   __shared__ typename Sum::Shared red;
   __shared__ typename Sum1::Shared red1;
   extern __shared__ __align__(128) char dyn[];
@@ -693,12 +708,15 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
   Sum1 sum1;
   const int cl = TPR > 32 ? p.cl : 1, rank = cl > 1 ? (int)cluster_rank() : 0;
   const int sub = threadIdx.x / TPR, tr = threadIdx.x % TPR;
-  const int c0 = rank * p.cols;
-  const int width = p.D - c0 < p.cols ? p.D - c0 : p.cols;  // this CTA's columns
   const float inv = 1.f / (float)p.D;
   const T *y = static_cast<const T *>(p.y);
   const int64_t step = (int64_t)(gridDim.x / cl) * RPC;
   const int64_t first = (int64_t)(blockIdx.x / cl) * RPC;
+  // this CTA's places: `cols` of them from c0 on, of which [lo, hi) are columns
+  const int lead = ODD ? (int)((first + sub) % 8) * (p.D % 8) % 8 : 0;
+  const int c0 = rank * p.cols;
+  const int lo = ODD && lead > c0 ? lead - c0 : 0;
+  const int hi = lead + p.D - c0 < p.cols ? lead + p.D - c0 : p.cols;
   __shared__ int gave_up;
   volatile int *abort = &gave_up;
   if constexpr (TPR > 32) {
@@ -709,78 +727,80 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
     if (cl > 1) cluster_arrive_wait();  // every CTA's barriers are there
   }
 
-  // unit n: its first column, and moves of its eight values
-  auto col = [&](int n) { return ONE ? n * 8 * TPR + tr : (n * TPR + tr) * 8; };
-  auto get_shared = [&](auto &raw, const auto *row, int c) {
-    if constexpr (ONE) raw.load_strided(row + c, TPR, width - c);
-    else raw.load_shared(row + c);
-  };
+  // unit n: its first place; whether it holds columns, and only columns
+  auto col = [&](int n) { return (n * TPR + tr) * 8; };
+  auto on = [&](int c) { return c < hi && (!ODD || c + 8 > lo); };
+  auto whole = [&](int c) { return !ODD || (c >= lo && c + 8 <= hi); };
   auto put = [&](auto *row, int c, const float2 (&x)[P]) {
-    if constexpr (ONE) store_strided(row + c, x, TPR, width - c);
-    else store_pairs(row + c, x);
+    if (whole(c)) store_pairs(row + c, x);
+    else store_some(row + c, x, lo - c, hi - c);
   };
-  // weights (0: w, 1: pw) of a unit.  In shared memory the first and the last
-  // four of a unit of neighbours lie apart, so that a warp reads whole lines.
+  auto take_shared = [&](auto &raw, const auto *row, int c) {
+    raw.load_shared(row + c);
+    if (!whole(c)) raw.keep(lo - c, hi - c);
+  };
+  auto take = [&](auto &raw, const auto *row, int c) {
+    if (whole(c)) raw.load(row + c);
+    else raw.load_some(row + c, lo - c, hi - c);
+  };
+  // the weights (0: w, 1: pw) of a unit from memory
+  auto weights_of = [&](int which, int c, float2 (&x)[P]) {
+    const float *w = which ? p.post_weight : p.weight;
+    if (w) w += c0 + c - lead;
+    if (!ODD) weights8(w, x);
+    else weights_some(w, x, lo - c, hi - c);
+  };
+  // and from where they are kept: a warp's in registers; else in shared
+  // memory, the first four and the last four of a unit apart, so that a warp
+  // reads whole lines
+  float2 mine[RING ? 1 : POST ? 2 : 1][RING ? 1 : NV][P];
   float4 *held = reinterpret_cast<float4 *>(dyn + kRingHead);
-  const int units = p.cols / 8, room = (p.cols + 3) / 4 * 4;
-  auto weights = [&](int which, int c, float2 (&x)[P]) {
-    if constexpr (RING && ONE) {
-      weights_strided(reinterpret_cast<float *>(held) + which * room + c, x, TPR, width - c);
-    } else if constexpr (RING) {
-      const float4 a = held[2 * which * units + c / 8], b = held[(2 * which + 1) * units + c / 8];
+  const int units = p.cols / 8;
+  auto weights = [&](int which, int n, float2 (&x)[P]) {
+    if constexpr (RING) {
+      const int u = col(n) / 8;
+      const float4 a = held[2 * which * units + u], b = held[(2 * which + 1) * units + u];
       x[0] = make_float2(a.x, a.y);
       x[1] = make_float2(a.z, a.w);
       x[2] = make_float2(b.x, b.y);
       x[3] = make_float2(b.z, b.w);
     } else {
-      const float *w = which ? p.post_weight : p.weight;
-      weights8(w ? w + c : w, x);
+      copy(mine[which][n], x);
     }
   };
 
-  // A stage of the ring: h | dh' | dn | y, the ones that are.  A bulk copy
-  // moves whole 16-byte pieces: where rows (ONE) begin or end inside one, the
-  // pieces around the row are copied and it is read from `lead` bytes on; the
-  // last pieces of the whole tensor, of which bytes lie behind its end, come
-  // value by value.
+  // a stage of the ring: h | dh' | dn | y, the ones that are
   const int64_t total = p.rows * p.D;
   const bool has_g = GRAD && p.dh_new, has_y = HAS_Y && y;
   const uint32_t bars = smem_u32(dyn);
-  const uint32_t hb = row_room<R, ONE>(p.cols), yb = row_room<T, ONE>(p.cols);
+  const uint32_t hb = p.cols * sizeof(R), yb = p.cols * sizeof(T);
   const uint32_t at_g = hb, at_s = at_g + (has_g ? hb : 0), at_y = at_s + (GRAD ? yb : 0);
   const uint32_t stage_bytes = at_y + (has_y ? yb : 0);
-  char *ring = dyn + kRingHead + (POST ? 2 : 1) * sizeof(float) * room;
-  auto lead = [&](int64_t at, int es) { return ONE ? (uint32_t)(at * es) & 15u : 0u; };
-  auto fetch_one = [&](const auto *x, int64_t at, char *to, uint32_t bar) -> uint32_t {
+  char *ring = dyn + kRingHead + (POST ? 2 : 1) * sizeof(float) * p.cols;
+  // Whole pieces from place 0 on.  Behind the end of the tensor (the last row
+  // of ODD ones) the values of the last piece come one by one instead.
+  auto fetch_one = [&](const auto *x, int64_t at, int n, char *to, uint32_t bar) -> uint32_t {
     using X = typename std::remove_const<typename std::remove_pointer<decltype(x)>::type>::type;
-    constexpr int es = sizeof(X);
-    if constexpr (!ONE) {
-      bulk_row(smem_u32(to), x + at, (uint32_t)width * es, bar);
-      return 0;
-    } else {
-      const char *from = reinterpret_cast<const char *>(x + at) - lead(at, es);
-      uint32_t bytes = (lead(at, es) + (uint32_t)width * es + 15u) / 16u * 16u;
-      if (from + bytes > reinterpret_cast<const char *>(x + total)) {
-        bytes -= 16;
-        const int first = ((int)bytes - (int)lead(at, es)) / es;  // the first column not copied
-        X *s = reinterpret_cast<X *>(to + bytes);
-        for (int i = first < 0 ? -first : 0; first + i < width; i++) s[i] = x[at + first + i];
-      }
-      if (bytes) bulk_row(smem_u32(to), from, bytes, bar);
-      return bytes;
+    constexpr int PIECE = 16 / sizeof(X);
+    if (ODD && at + n > total) {
+      n = (int)(total - at) / PIECE * PIECE;
+      for (int i = n; i < hi; i++) reinterpret_cast<X *>(to)[i] = x[at + i];
     }
+    if (!ODD || n) bulk_row(smem_u32(to), x + at, (uint32_t)(n * sizeof(X)), bar);
+    return (uint32_t)(n * sizeof(X));
   };
   auto fetch = [&](int64_t row, int st) {  // thread 0
     const uint32_t bar = bars + st * 8;
     char *to = ring + st * stage_bytes;
-    const int64_t at = row * p.D + c0;
-    if constexpr (!ONE)
-      mbar_expect_tx(bar, (uint32_t)width * ((has_g ? 2 : 1) * sizeof(R) + (GRAD + has_y) * sizeof(T)));
-    uint32_t bytes = fetch_one(static_cast<const R *>(p.h), at, to, bar);
-    if (has_g) bytes += fetch_one(static_cast<const R *>(p.dh_new), at, to + at_g, bar);
-    if (GRAD) bytes += fetch_one(static_cast<const T *>(p.dn), at, to + at_s, bar);
-    if (has_y) bytes += fetch_one(y, at, to + at_y, bar);
-    if constexpr (ONE) mbar_expect_tx(bar, bytes);
+    const int64_t at = row * p.D - lead + c0;
+    const int n = ODD ? (hi + 7) / 8 * 8 : hi;
+    if constexpr (!ODD)
+      mbar_expect_tx(bar, (uint32_t)hi * ((has_g ? 2 : 1) * sizeof(R) + (GRAD + has_y) * sizeof(T)));
+    uint32_t bytes = fetch_one(static_cast<const R *>(p.h), at, n, to, bar);
+    if (has_g) bytes += fetch_one(static_cast<const R *>(p.dh_new), at, n, to + at_g, bar);
+    if (GRAD) bytes += fetch_one(static_cast<const T *>(p.dn), at, n, to + at_s, bar);
+    if (has_y) bytes += fetch_one(y, at, n, to + at_y, bar);
+    if constexpr (ODD) mbar_expect_tx(bar, bytes);
   };
   if constexpr (RING) {
     if (threadIdx.x == 0) {
@@ -793,22 +813,28 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
       if (first < p.rows) fetch(first, 0);
       if (p.stages > 1 && first + step < p.rows) fetch(first + step, 1);
     }
-    for (int i = threadIdx.x; ONE && i < (POST ? 2 : 1) * room; i += NT) {
-      const int which = i >= room, c = i - which * room;
-      const float *w = which ? p.post_weight : p.weight;
-      reinterpret_cast<float *>(held)[i] = w && c < width ? __ldg(w + c0 + c) : 1.f;
-    }
-    for (int i = threadIdx.x; !ONE && i < (POST ? 2 : 1) * units; i += NT) {
+    for (int i = threadIdx.x; i < (POST ? 2 : 1) * units; i += NT) {
       const int which = i >= units, u = i - which * units;
-      const float *w = which ? p.post_weight : p.weight;
-      if (u * 8 < width) {
+      if (on(u * 8)) {
         float2 x[P];
-        weights8(w ? w + c0 + u * 8 : w, x);
+        weights_of(which, u * 8, x);
         held[2 * which * units + u] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
         held[(2 * which + 1) * units + u] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
       }
     }
     __syncthreads();
+  } else {
+#pragma unroll
+    for (int k = 0; k < (POST ? 2 : 1); k++)
+#pragma unroll
+      for (int n = 0; n < NV; n++) {
+        if (on(col(n))) {
+          weights_of(k, col(n), mine[k][n]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < P; i++) mine[k][n][i] = pair(0.f);
+        }
+      }
   }
   const int shift = p.stages - 1;
 
@@ -827,7 +853,7 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
   for (int64_t r0 = first; r0 < p.rows; r0 += step, it++) {
     const int64_t row = r0 + sub;
     const bool live = row < p.rows;
-    const int64_t at = row * p.D + c0;
+    const int64_t at = row * p.D - lead + c0;
     RowData<T, R, GRAD, POST, NV> d;
     const int st = (int)it & shift;
     const char *stage = ring + st * stage_bytes;
@@ -837,27 +863,26 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
 #pragma unroll
     for (int n = 0; n < NV; n++) {
       const int c = col(n);
-      if (live && c < width) {
+      if (live && on(c)) {
         if constexpr (RING) {
-          const char *hr = stage + lead(at, sizeof(R)), *yr = stage + lead(at, sizeof(T));
-          get_shared(d.h[n], reinterpret_cast<const R *>(hr), c);
+          take_shared(d.h[n], reinterpret_cast<const R *>(stage), c);
           if constexpr (GRAD) {
-            if (has_g) get_shared(d.g[n], reinterpret_cast<const R *>(hr + at_g), c);
+            if (has_g) take_shared(d.g[n], reinterpret_cast<const R *>(stage + at_g), c);
             else d.g[n].clear();
-            get_shared(d.s[n], reinterpret_cast<const T *>(yr + at_s), c);
+            take_shared(d.s[n], reinterpret_cast<const T *>(stage + at_s), c);
           }
           if constexpr (HAS_Y) {
-            if (has_y) get_shared(d.y[n], reinterpret_cast<const T *>(yr + at_y), c);
+            if (has_y) take_shared(d.y[n], reinterpret_cast<const T *>(stage + at_y), c);
           }
         } else {
-          d.h[n].load(static_cast<const R *>(p.h) + at + c);
+          take(d.h[n], static_cast<const R *>(p.h) + at, c);
           if constexpr (GRAD) {
-            if (has_g) d.g[n].load(static_cast<const R *>(p.dh_new) + at + c);
+            if (has_g) take(d.g[n], static_cast<const R *>(p.dh_new) + at, c);
             else d.g[n].clear();
-            d.s[n].load(static_cast<const T *>(p.dn) + at + c);
+            take(d.s[n], static_cast<const T *>(p.dn) + at, c);
           }
           if constexpr (HAS_Y) {
-            if (has_y) d.y[n].load(y + at + c);
+            if (has_y) take(d.y[n], y + at, c);
           }
         }
       } else {
@@ -903,10 +928,10 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
 #pragma unroll
         for (int n = 0; n < NV; n++) {
           const int c = col(n);
-          if (!(live && c < width)) continue;
+          if (!(live && on(c))) continue;
           float2 z[P], w[P];
           d.y[n].get2(z);
-          if constexpr (POST) weights(1, c, w);
+          if constexpr (POST) weights(1, n, w);
 #pragma unroll
           for (int i = 0; i < P; i++) {
             if constexpr (POST) z[i] = mul2(z[i], w[i]);
@@ -927,9 +952,9 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
 #pragma unroll
       for (int n = 0; n < NV; n++) {
         const int c = col(n);
-        if (!(live && c < width)) continue;
+        if (!(live && on(c))) continue;
         float2 w[P];
-        weights(0, c, w);
+        weights(0, n, w);
 #pragma unroll
         for (int i = 0; i < P; i++) w[i] = mul2(w[i], mul2(x[n][i], rstd));
         put(static_cast<T *>(p.n) + at, c, w);
@@ -940,9 +965,9 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
 #pragma unroll
       for (int n = 0; n < NV; n++) {
         const int c = col(n);
-        if (c >= width) continue;
+        if (!on(c)) continue;
         float2 w[P], x[P], s[P];
-        weights(0, c, w);
+        weights(0, n, w);
         d.h[n].get2(x);
         d.s[n].get2(s);
 #pragma unroll
@@ -968,9 +993,9 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
 #pragma unroll
       for (int n = 0; n < NV; n++) {
         const int c = col(n);
-        if (!(live && c < width)) continue;
+        if (!(live && on(c))) continue;
         float2 w[P], x[P], s[P], g[P];
-        weights(0, c, w);
+        weights(0, n, w);
         d.h[n].get2(x);
         d.s[n].get2(s);
         d.g[n].get2(g);
@@ -986,7 +1011,7 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
         if constexpr (POST) {
           float2 z[P];
           d.y[n].get2(z);
-          weights(1, c, w);
+          weights(1, n, w);
 #pragma unroll
           for (int i = 0; i < P; i++) {
             const float2 yn = mul2(z[i], ry);
@@ -1006,7 +1031,7 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
 #pragma unroll
         for (int n = 0; n < NV; n++) {
           const int c = col(n);
-          if (!(live && c < width)) continue;
+          if (!(live && on(c))) continue;
           if constexpr (POST) {
             float2 z[P];
             d.y[n].get2(z);
@@ -1034,25 +1059,26 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
     const int64_t group = blockIdx.x / cl;
     auto flush = [&](float *to, const float2 (&acc)[NV][P]) {
       if (!to) return;
-      to += group * p.D + c0;
+      to += group * p.D;
       if constexpr (RPC == 1) {
 #pragma unroll
         for (int n = 0; n < NV; n++) {
           const int c = col(n);
-          if (c < width) put(to, c, acc[n]);
+          if (on(c)) put(to + (c0 - lead), c, acc[n]);
         }
       } else {
-        float2 *acc_s = reinterpret_cast<float2 *>(dyn);
+        float *acc_s = reinterpret_cast<float *>(dyn) + sub * p.D;
         __syncthreads();
 #pragma unroll
-        for (int n = 0; n < NV; n++)
-#pragma unroll
-          for (int i = 0; i < P; i++) acc_s[(sub * NV * TPR + n * TPR + tr) * P + i] = acc[n][i];
+        for (int n = 0; n < NV; n++) {
+          const int c = col(n);
+          if (on(c)) store_some(acc_s - lead + c, acc[n], lo - c, hi - c);
+        }
         __syncthreads();
-        for (int c = threadIdx.x; c < width; c += NT) {
+        for (int c = threadIdx.x; c < p.D; c += NT) {
           float a = 0.f;
 #pragma unroll
-          for (int k = 0; k < RPC; k++) a += reinterpret_cast<float *>(dyn)[k * (TPR * NV * 8) + c];
+          for (int k = 0; k < RPC; k++) a += reinterpret_cast<float *>(dyn)[k * p.D + c];
           to[c] = a;
         }
       }

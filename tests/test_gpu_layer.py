@@ -342,6 +342,9 @@ RESIDUAL = [
     (7, 520, BF, BF, False, True), (601, 1111, FP, FP, False, True), (33, 2049, BF, FP, True, True),
     (1300, 256, BF, BF, True, True), (65, 4096, BF, BF, False, True), (9, 4096, BF, FP, True, True),
     (9, 4104, FP, FP, True, True), (5, 16384, BF, BF, True, True), (4, 16384, FP, FP, True, True),
+    (5003, 99, BF, FP, True, True), (2600, 505, FP, FP, True, True), (4001, 3, BF, BF, False, True),
+    (901, 1700, BF, BF, False, True), (400, 5001, BF, BF, True, True), (350, 4095, BF, FP, True, True),
+    (340, 9001, FP, FP, False, True), (5, 4097, BF, BF, True, True), (2, 2043, BF, FP, True, False),
     (3, 16383, BF, FP, True, True), (3, 16383, FP, FP, False, False), (700, 8192, BF, FP, False, True),
 ]
 
