@@ -795,7 +795,7 @@ cudaError_t gated_call(const la2::norm::Gated &p, la2_dtype dt, unsigned flags, 
 // What two residual norm's CTAs on an SM may each have: half of its shared
 // memory less what the system and the kernel's static arrays take.
 constexpr size_t two_ctas(bool grad, bool odd) {
-  return 233472 / 2 - 1024 - (grad ? 1200 : 640) * (odd ? 2 : 1);
+  return 233472 / 2 - 1024 - (grad ? 1664 : 384) * (odd ? 2 : 1);
 }
 // Shared memory of such a CTA: the weights and `stages` rows of the streams
 // that there are.

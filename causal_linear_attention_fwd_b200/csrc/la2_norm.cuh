@@ -699,13 +699,10 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
   constexpr bool HAS_Y = !GRAD || POST;  // y may be read
   constexpr int RPC = NT / TPR, P = 4;
   // 16,384 columns take four CTAs, the up to 7 places more of odd rows eight
-  using Sum = RowSum<TPR, GRAD ? 3 : 1, ODD ? 8 : 4>;
-  using Sum1 = RowSum<TPR, 1, ODD ? 8 : 4>;
+  using Sum = RowSum<TPR, !GRAD ? 1 : POST ? 6 : 2, ODD ? 8 : 4>;
   __shared__ typename Sum::Shared red;
-  __shared__ typename Sum1::Shared red1;
   extern __shared__ __align__(128) char dyn[];
   Sum sum;
-  Sum1 sum1;
   const int cl = TPR > 32 ? p.cl : 1, rank = cl > 1 ? (int)cluster_rank() : 0;
   const int sub = threadIdx.x / TPR, tr = threadIdx.x % TPR;
   const float inv = 1.f / (float)p.D;
@@ -722,7 +719,6 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
   if constexpr (TPR > 32) {
     if (threadIdx.x == 0) gave_up = 0;
     sum.init(red, cl);
-    sum1.init(red1, cl);
     __syncthreads();
     if (cl > 1) cluster_arrive_wait();  // every CTA's barriers are there
   }
@@ -919,7 +915,7 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
             for (int i = 0; i < P; i++) q2 = fma2(z[i], z[i], q2);
           }
           float q[1] = {q2.x + q2.y};
-          sum1(q, red1, cl, rank, abort);
+          sum(q, red, cl, rank, abort);
           refill();
           refilled = true;
           ry = pair(rsqrtf(fmaf(q[0], inv, p.eps)) * p.beta);
@@ -960,36 +956,55 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
         put(static_cast<T *>(p.n) + at, c, w);
       }
     } else {
-      // sums of h'^2, (dn w) h' and, with a norm on y, y^2
-      float2 q0 = pair(0.f), q1 = pair(0.f), q2 = pair(0.f);
+      // Sums of h'^2, s h' and, with a norm on y, of y^2 and pw y times each of
+      // dh', s and h': dH is a combination of these three whose factors the
+      // first sums give, so the mean that dy needs comes out of the same
+      // reduction.
+      float2 q2[POST ? 6 : 2];
+#pragma unroll
+      for (int i = 0; i < (POST ? 6 : 2); i++) q2[i] = pair(0.f);
 #pragma unroll
       for (int n = 0; n < NV; n++) {
-        const int c = col(n);
-        if (!on(c)) continue;
+        if (!on(col(n))) continue;
         float2 w[P], x[P], s[P];
         weights(0, n, w);
         d.h[n].get2(x);
         d.s[n].get2(s);
 #pragma unroll
         for (int i = 0; i < P; i++) {
-          q0 = fma2(x[i], x[i], q0);
-          q1 = fma2(mul2(s[i], w[i]), x[i], q1);
+          s[i] = mul2(s[i], w[i]);
+          q2[0] = fma2(x[i], x[i], q2[0]);
+          q2[1] = fma2(s[i], x[i], q2[1]);
         }
         if constexpr (POST) {
-          float2 z[P];
+          float2 z[P], g[P];
           d.y[n].get2(z);
+          d.g[n].get2(g);
+          weights(1, n, w);
 #pragma unroll
-          for (int i = 0; i < P; i++) q2 = fma2(z[i], z[i], q2);
+          for (int i = 0; i < P; i++) {
+            const float2 pz = mul2(z[i], w[i]);
+            q2[2] = fma2(z[i], z[i], q2[2]);
+            q2[3] = fma2(pz, g[i], q2[3]);
+            q2[4] = fma2(pz, s[i], q2[4]);
+            q2[5] = fma2(pz, x[i], q2[5]);
+          }
         }
       }
-      float q[3] = {q0.x + q0.y, q1.x + q1.y, q2.x + q2.y};
+      float q[POST ? 6 : 2];
+#pragma unroll
+      for (int i = 0; i < (POST ? 6 : 2); i++) q[i] = q2[i].x + q2[i].y;
       sum(q, red, cl, rank, abort);
       refill();
-      const float r = rsqrtf(fmaf(q[0], inv, p.eps));
-      const float2 rstd = pair(r), m = pair(-q[1] * r * inv);  // -mean(s hn)
-      const float2 ry = pair(POST ? rsqrtf(fmaf(q[2], inv, p.eps)) : 1.f);
+      const float r = rsqrtf(fmaf(q[0], inv, p.eps)), mean = -q[1] * r * inv;  // -mean(s hn)
+      const float2 rstd = pair(r), m = pair(mean);
       const float2 al = pair(p.alpha), be = pair(p.beta);
-      float2 k = pair(0.f), dp[NV][P];       // k: sum of (dp pw) yn
+      float2 ry = pair(1.f), mz = pair(0.f);  // mz: -mean((dp pw) yn) / rms(y)
+      if constexpr (POST) {
+        const float y1 = rsqrtf(fmaf(q[2], inv, p.eps));
+        ry = pair(y1);
+        mz = pair(-p.beta * y1 * y1 * inv * fmaf(r, fmaf(mean * r, q[5], q[4]), q[3]));
+      }
 #pragma unroll
       for (int n = 0; n < NV; n++) {
         const int c = col(n);
@@ -1005,7 +1020,7 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
           aw[n][i] = fma2(s[i], hn, aw[n][i]);
           const float2 dH = fma2(rstd, fma2(hn, m, mul2(s[i], w[i])), g[i]);
           x[i] = mul2(al, dH);
-          dp[n][i] = mul2(be, dH);
+          g[i] = mul2(be, dH);  // dp
         }
         put(static_cast<R *>(p.dh) + at, c, x);
         if constexpr (POST) {
@@ -1014,32 +1029,11 @@ __global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__
           weights(1, n, w);
 #pragma unroll
           for (int i = 0; i < P; i++) {
-            const float2 yn = mul2(z[i], ry);
-            ap[n][i] = fma2(dp[n][i], yn, ap[n][i]);
-            dp[n][i] = mul2(dp[n][i], w[i]);
-            k = fma2(dp[n][i], yn, k);
+            ap[n][i] = fma2(g[i], mul2(z[i], ry), ap[n][i]);
+            g[i] = mul2(ry, fma2(z[i], mz, mul2(g[i], w[i])));
           }
         }
-      }
-      if (p.dy) {
-        float2 mz = pair(0.f);               // -mean((dp pw) yn) / rms(y)
-        if constexpr (POST) {
-          float t[1] = {k.x + k.y};
-          sum1(t, red1, cl, rank, abort);
-          mz = mul2(pair(-t[0] * inv), ry);
-        }
-#pragma unroll
-        for (int n = 0; n < NV; n++) {
-          const int c = col(n);
-          if (!(live && on(c))) continue;
-          if constexpr (POST) {
-            float2 z[P];
-            d.y[n].get2(z);
-#pragma unroll
-            for (int i = 0; i < P; i++) dp[n][i] = mul2(ry, fma2(z[i], mz, dp[n][i]));
-          }
-          put(static_cast<T *>(p.dy) + at, c, dp[n]);
-        }
+        if (p.dy) put(static_cast<T *>(p.dy) + at, c, g);
       }
     }
   }
