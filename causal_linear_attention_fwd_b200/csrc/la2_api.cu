@@ -642,7 +642,9 @@ NormPlan row_plan(int D, bool odd, int most_units = 2) {
   NormPlan g;
   g.slices = 1;
   g.odd = odd;
-  const int places = odd ? D + 7 : D, most = 2048 * most_units;
+  const int places = odd ? D + 7 : D;
+  // 256 threads to a CTA, or 512 where that saves a cluster (two units each)
+  const int threads = most_units == 2 && places > 4096 ? 512 : 256, most = 8 * threads * most_units;
   g.cl = 1;
   while (g.cl * most < places) g.cl *= 2;
   g.cols = ((places + 7) / 8 + g.cl - 1) / g.cl * 8;
@@ -654,8 +656,8 @@ NormPlan row_plan(int D, bool odd, int most_units = 2) {
     g.nt = g.tpr = 128;
     g.nv = 1;
   } else {
-    g.nt = g.tpr = 256;
-    g.nv = g.cols <= 2048 ? 1 : g.cols <= 4096 ? 2 : 4;
+    g.nt = g.tpr = threads;
+    g.nv = g.cols <= 2048 ? 1 : g.cols <= 16 * threads ? 2 : 4;
   }
   g.rpc = g.nt / g.tpr;
   return g;
@@ -775,6 +777,7 @@ cudaError_t gated_shape(const la2::norm::Gated &p, bool row, float *dw, cudaStre
   if (g.tpr == 32) return gated_launch<T, 0, true, GRAD, GATE, 128, 32, 2>(p, g, dw, st);
   if (g.tpr == 128) return gated_launch<T, 0, true, GRAD, GATE, 128, 128, 1>(p, g, dw, st);
   if (g.nv == 1) return gated_launch<T, 0, true, GRAD, GATE, 256, 256, 1>(p, g, dw, st);
+  if (g.tpr == 512) return gated_launch<T, 0, true, GRAD, GATE, 512, 512, 2>(p, g, dw, st);
   return gated_launch<T, 0, true, GRAD, GATE, 256, 256, 2>(p, g, dw, st);
 }
 template <typename T, bool GRAD>
@@ -814,8 +817,10 @@ cudaError_t residual_launch(la2::norm::Residual p, const NormPlan &g, float *dw,
   size_t smem = 0;
   p.stages = 1;
   if (TPR > 32) {
-    // two rows where two CTAs on an SM have room for them, else one
-    p.stages = residual_smem<T, R, POST, GRAD>(p, g.cols, 2) <= two_ctas(GRAD, ODD) ? 2 : 1;
+    // two rows where two CTAs on an SM (one of 512 threads) have room for
+    // them, else one
+    const size_t room = NT == 512 ? 232448 - 3072 : two_ctas(GRAD, ODD);
+    p.stages = residual_smem<T, R, POST, GRAD>(p, g.cols, 2) <= room ? 2 : 1;
     smem = residual_smem<T, R, POST, GRAD>(p, g.cols, p.stages);
   } else if (GRAD) {
     smem = (size_t)(NT / TPR) * p.D * sizeof(float);
@@ -842,6 +847,7 @@ cudaError_t residual_shape(const la2::norm::Residual &p, float *dw, float *dpw, 
     const NormPlan g = row_plan(p.D, true);
     if (g.tpr == 32) return residual_launch<T, R, POST, GRAD, true, 128, 32, 2>(p, g, dw, dpw, st);
     if (g.nv == 1) return residual_launch<T, R, POST, GRAD, true, 256, 256, 1>(p, g, dw, dpw, st);
+    if (g.tpr == 512) return residual_launch<T, R, POST, GRAD, true, 512, 512, 2>(p, g, dw, dpw, st);
     return residual_launch<T, R, POST, GRAD, true, 256, 256, 2>(p, g, dw, dpw, st);
   }
   NormPlan g = row_plan(p.D, false, GRAD ? 2 : 4);
@@ -853,6 +859,7 @@ cudaError_t residual_shape(const la2::norm::Residual &p, float *dw, float *dpw, 
   if (g.nv == 1) return residual_launch<T, R, POST, GRAD, false, 256, 256, 1>(p, g, dw, dpw, st);
   if constexpr (!GRAD)
     if (g.nv == 4) return residual_launch<T, R, POST, GRAD, false, 256, 256, 4>(p, g, dw, dpw, st);
+  if (g.tpr == 512) return residual_launch<T, R, POST, GRAD, false, 512, 512, 2>(p, g, dw, dpw, st);
   return residual_launch<T, R, POST, GRAD, false, 256, 256, 2>(p, g, dw, dpw, st);
 }
 

@@ -273,7 +273,7 @@ struct RowSum {
   static constexpr int NW = TPR / 32;
   struct Shared {
     uint64_t bars[2];
-    float red[2][K][TPR > 32 ? MAXCL * NW : 1];
+    float red[2][K][TPR > 32 ? (MAXCL * NW > 64 ? 64 : MAXCL * NW) : 1];
   };
   uint32_t uses = 0;
   // before the first sum, by all threads; a barrier of the CTA (cl = 1: none
@@ -366,8 +366,8 @@ template <bool GRAD, Gate GATE>
 constexpr int gated_streams() { return 1 + GRAD + (GATE != GATE_NONE); }
 template <typename T, int NV>
 constexpr int gated_stages() { return NV == 2 ? 2 : 3; }
-template <typename T, bool GRAD, int NV>
-constexpr int gated_ctas() { return GRAD || sizeof(T) == 4 ? 2 : 4; }
+template <typename T, bool GRAD, int NT>
+constexpr int gated_ctas() { return (GRAD || sizeof(T) == 4 ? 2 : 4) / (NT == 512 ? 2 : 1); }
 template <typename T, bool GRAD, Gate GATE, int NT, int NV>
 constexpr size_t gated_smem() {
   const size_t ring = (size_t)NT * NV * 8 * sizeof(T) * gated_streams<GRAD, GATE>() * gated_stages<T, NV>();
@@ -381,7 +381,7 @@ constexpr size_t gated_smem() {
 // (heads; slice blockIdx.y) and NT >> tpr_shift tokens; ROW, a warp or the
 // CTA per row, NV vectors each, slice = the CTA's rank in its cluster.
 template <typename T, int E, bool ROW, bool GRAD, Gate GATE, int NT, int TPR, int NV>
-__global__ void __launch_bounds__(NT, gated_ctas<T, GRAD, NV>())
+__global__ void __launch_bounds__(NT, gated_ctas<T, GRAD, NT>())
 gated_kernel(const __grid_constant__ Gated p) {
   constexpr int V = 8, P = V / 2, LPH = ROW ? 32 : E / V;
   constexpr int S = gated_stages<T, NV>();
@@ -694,7 +694,7 @@ struct RowData {
 
 // TPR threads hold a row, NV units each.
 template <typename T, typename R, bool GRAD, bool POST, bool ODD, int NT, int TPR, int NV>
-__global__ void __launch_bounds__(NT, 2) residual_kernel(const __grid_constant__ Residual p) {
+__global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) residual_kernel(const __grid_constant__ Residual p) {
   constexpr bool RING = TPR > 32;
   constexpr bool HAS_Y = !GRAD || POST;  // y may be read
   constexpr int RPC = NT / TPR, P = 4;
