@@ -84,6 +84,15 @@ template <typename T> struct Raw {
       r[0] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
   }
+  // all eight at any alignment, the last four from p + apart on
+  __device__ __forceinline__ void load_any(const T *p, int apart) {
+    load_some(p, 0, 4);
+    Raw<T> q;
+    q.load_some(p + apart - 4, 4, 8);
+#pragma unroll
+    for (int i = 0; i < N; i++)
+      r[i] = make_uint4(r[i].x | q.r[i].x, r[i].y | q.r[i].y, r[i].z | q.r[i].z, r[i].w | q.r[i].w);
+  }
   // all but the values lo <= i < hi set to 0
   __device__ __forceinline__ void keep(int lo, int hi) {
     uint32_t m[8];
@@ -123,14 +132,14 @@ template <typename T> struct Raw {
 };
 
 template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&f)[8]) {
+__device__ __forceinline__ void store8(T *p, const float (&f)[8], int apart = 4) {
   constexpr int N = fmap::vec16<T>::N;
 #pragma unroll
   for (int i = 0; i < 8 / N; i++) {
     float g[N];
 #pragma unroll
     for (int j = 0; j < N; j++) g[j] = f[i * N + j];
-    fmap::st_stream(p + i * N, fmap::vec16<T>::pack(g));
+    fmap::st_stream(p + i * apart, fmap::vec16<T>::pack(g));
   }
 }
 // the values lo <= i < hi alone
@@ -140,21 +149,26 @@ __device__ __forceinline__ void store_some(T *p, const float2 (&x)[4], int lo, i
   for (int i = 0; i < 8; i++)
     if (i >= lo && i < hi) io<T>::st(p + i, i % 2 ? x[i / 2].y : x[i / 2].x);
 }
+// apart: from the first to the fifth value (4: neighbours)
 template <typename T>
-__device__ __forceinline__ void store_pairs(T *p, const float2 (&x)[4]) {
+__device__ __forceinline__ void store_pairs(T *p, const float2 (&x)[4], int apart = 4) {
   float f[8];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     f[2 * i] = x[i].x;
     f[2 * i + 1] = x[i].y;
   }
-  store8(p, f);
+  store8(p, f, apart);
 }
 // vec: the address is 16-byte aligned (else the element's alignment only)
 template <typename T>
-__device__ __forceinline__ void store_any(T *p, const float2 (&x)[4], bool vec) {
-  if (vec) store_pairs(p, x);
-  else store_some(p, x, 0, 8);
+__device__ __forceinline__ void store_any(T *p, const float2 (&x)[4], bool vec, int apart) {
+  if (vec) {
+    store_pairs(p, x, apart);
+  } else {
+    store_some(p, x, 0, 4);
+    store_some(p + apart - 4, x, 4, 8);
+  }
 }
 // 16 bytes into shared memory, behind the thread's back.
 __device__ __forceinline__ void copy16_async(void *to, const void *from) {
@@ -166,12 +180,13 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 // Weights: fp32 (null: ones), read by every row of a CTA, so through the cache.
-__device__ __forceinline__ void weights8(const float *w, float2 (&f)[4]) {
+__device__ __forceinline__ void weights8(const float *w, float2 (&f)[4], int apart = 4) {
   if (!w) {
 #pragma unroll
     for (int i = 0; i < 4; i++) f[i] = make_float2(1.f, 1.f);
   } else {
-    const float4 x = __ldg(reinterpret_cast<const float4 *>(w)), y = __ldg(reinterpret_cast<const float4 *>(w) + 1);
+    const float4 x = __ldg(reinterpret_cast<const float4 *>(w));
+    const float4 y = __ldg(reinterpret_cast<const float4 *>(w + apart));
     f[0] = make_float2(x.x, x.y);
     f[1] = make_float2(x.z, x.w);
     f[2] = make_float2(y.x, y.y);
@@ -384,6 +399,9 @@ template <typename T, int E, bool ROW, bool GRAD, Gate GATE, int NT, int TPR, in
 __global__ void __launch_bounds__(NT, gated_ctas<T, GRAD, NT>())
 gated_kernel(const __grid_constant__ Gated p) {
   constexpr int V = 8, P = V / 2, LPH = ROW ? 32 : E / V;
+  // a unit: 8 neighbours, or in fp32 twice 4 of them, 32 columns apart, so that
+  // 8 lanes move whole lines
+  constexpr int APART = sizeof(T) == 2 ? 4 : 32;
   constexpr int S = gated_stages<T, NV>();
   constexpr bool HOLD = !(GRAD && NV == 2);  // the weights, in registers throughout
   using Sum = RowSum<ROW ? TPR : 32, GRAD ? 2 : 1, 4>;
@@ -412,7 +430,7 @@ gated_kernel(const __grid_constant__ Gated p) {
   float2 held[HOLD ? NV : 1][P], acc[GRAD ? NV : 1][P];
   auto weights = [&](int col, float2 (&w)[P]) {
     if (col < end) {
-      weights8(p.weight ? p.weight + (p.shared ? col % e : col) : nullptr, w);
+      weights8(p.weight ? p.weight + (p.shared ? col % e : col) : nullptr, w, APART);
     } else {
 #pragma unroll
       for (int i = 0; i < P; i++) w[i] = pair(0.f);
@@ -420,7 +438,7 @@ gated_kernel(const __grid_constant__ Gated p) {
   };
 #pragma unroll
   for (int n = 0; n < NV; n++) {
-    c[n] = c0 + (n * tpr + tr) * V;
+    c[n] = c0 + (sizeof(T) == 2 ? (n * tpr + tr) * V : (n * tpr + tr) / 8 * 64 + tr % 8 * 4);
     at_o[n] = (int64_t)(c[n] / e) * p.L * e + c[n] % e;
     if constexpr (HOLD) weights(c[n], held[n]);
     if constexpr (GRAD) {
@@ -481,9 +499,9 @@ gated_kernel(const __grid_constant__ Gated p) {
         const T *up = static_cast<const T *>(p.du) + a.row * D + c[n];
 #pragma unroll
         for (int i = 0; i < N; i++) {
-          copy16_async(slot(stage, 0, n, i), reinterpret_cast<const uint4 *>(x) + i);
-          if (GRAD) copy16_async(slot(stage, 1, n, i), reinterpret_cast<const uint4 *>(up) + i);
-          if (gate_ahead) copy16_async(slot(stage, STREAMS - 1, n, i), reinterpret_cast<const uint4 *>(g) + i);
+          copy16_async(slot(stage, 0, n, i), x + i * APART);
+          if (GRAD) copy16_async(slot(stage, 1, n, i), up + i * APART);
+          if (gate_ahead) copy16_async(slot(stage, STREAMS - 1, n, i), g + i * APART);
         }
       }
     }
@@ -504,7 +522,7 @@ gated_kernel(const __grid_constant__ Gated p) {
             if (gate_ahead) cur.g[n].r[i] = *slot(stage, STREAMS - 1, n, i);
         }
         if constexpr (GATE != GATE_NONE)
-          if (!gate_ahead) cur.g[n].load_some(static_cast<const T *>(p.gate) + a.g + c[n], 0, 8);
+          if (!gate_ahead) cur.g[n].load_any(static_cast<const T *>(p.gate) + a.g + c[n], APART);
       } else {
         cur.x[n].clear();
         if constexpr (GATE != GATE_NONE) cur.g[n].clear();
@@ -586,7 +604,7 @@ gated_kernel(const __grid_constant__ Gated p) {
             if constexpr (GATE != GATE_NONE) x[i] = mul2(x[i], sigmoid2(g[i]));
             if constexpr (GATE == GATE_SILU) x[i] = mul2(x[i], g[i]);
           }
-          store_pairs(static_cast<T *>(p.u) + to.row * D + c[n], x);
+          store_pairs(static_cast<T *>(p.u) + to.row * D + c[n], x, APART);
         } else {
           const float2 m = pair(-sum[n][1] * rstd.x * inv);  // -mean(dy * y)
           float2 up[P], dg[P];
@@ -606,9 +624,9 @@ gated_kernel(const __grid_constant__ Gated p) {
             acc[n][i] = fma2(uy, pair(1.f), acc[n][i]);
             x[i] = mul2(rstd, fma2(y, m, dy));
           }
-          store_pairs(static_cast<T *>(p.d_o) + to.o + at_o[n], x);
+          store_pairs(static_cast<T *>(p.d_o) + to.o + at_o[n], x, APART);
           if constexpr (GATE != GATE_NONE)
-            store_any(static_cast<T *>(p.dgate) + to.dg + c[n], dg, p.dgate_vec);
+            store_any(static_cast<T *>(p.dgate) + to.dg + c[n], dg, p.dgate_vec, APART);
         }
       }
     }
@@ -634,8 +652,10 @@ gated_kernel(const __grid_constant__ Gated p) {
     for (int j = threadIdx.x; j < out; j += NT) {
       float sum = 0.f;
       for (int k = j; k < width; k += out) {
-        const int vec = k / V, n = vec / tpr, lane = vec % tpr;
-        for (int q = 0; q < rpc; q++) sum += acc_s[((q * tpr + lane) * NV + n) * V + k % V];
+        const int vec = sizeof(T) == 2 ? k / V : k / 64 * 8 + k % 32 / 4;
+        const int i = sizeof(T) == 2 ? k % V : k % 64 / 32 * 4 + k % 4;
+        const int n = vec / tpr, lane = vec % tpr;
+        for (int q = 0; q < rpc; q++) sum += acc_s[((q * tpr + lane) * NV + n) * V + i];
       }
       if (p.shared)
         p.dw[(group * gridDim.y + blockIdx.y) * e + j] = sum;
