@@ -931,11 +931,22 @@ bool apart(const la2_heads &x, int nx, int wx, const la2_heads &y, int ny, int w
   return side_by_side(wx, wy, {{x.batch, B}, {x.row, L}, {nx > 1 ? x.head : y.head, n}});
 }
 
-template <typename T, bool GRAD, bool INTER>
-void rotary_launch(const la2::rot::Args &a, dim3 grid, size_t smem, bool vec, cudaStream_t st) {
+template <typename T, bool GRAD, bool SUMS, bool INTER>
+void rotary_launch(const la2::rot::Args &a, dim3 grid, bool vec, cudaStream_t st) {
   using namespace la2::rot;
-  if (vec) rotary_kernel<T, GRAD, INTER, 8, sizeof(T) == 2 ? 4 : 2><<<grid, NT, smem, st>>>(a);
-  else rotary_kernel<T, GRAD, INTER, 1, 4><<<grid, NT, smem, st>>>(a);
+  const size_t smem = (size_t)TOK * (a.r / 2) * sizeof(float2) + (SUMS ? NT * 2 * (vec ? 8 : 1) * sizeof(float) : 0);
+  if (vec) rotary_kernel<T, GRAD, SUMS, INTER, 8, sizeof(T) == 2 ? 4 : 2><<<grid, NT, smem, st>>>(a);
+  else rotary_kernel<T, GRAD, SUMS, INTER, 1, 4><<<grid, NT, smem, st>>>(a);
+}
+template <typename T, bool GRAD>
+void rotary_form(const la2::rot::Args &a, bool inter, dim3 grid, bool vec, cudaStream_t st) {
+  if (GRAD && a.rep > 1) {
+    inter ? rotary_launch<T, GRAD, GRAD, true>(a, grid, vec, st)
+          : rotary_launch<T, GRAD, GRAD, false>(a, grid, vec, st);
+  } else {
+    inter ? rotary_launch<T, GRAD, false, true>(a, grid, vec, st)
+          : rotary_launch<T, GRAD, false, false>(a, grid, vec, st);
+  }
 }
 
 template <bool GRAD>
@@ -971,7 +982,7 @@ la2_status rotary_call(const la2_heads *q, const la2_heads *k, const la2_heads *
     out[i] = {major[i], (size_t)B * H * L * width[i] * es};
     const int64_t odd = (B > 1 ? x.batch : 0) | (n[i] > 1 ? x.head : 0) | (L > 1 ? x.row : 0);
     vec = vec && aligned16(x.p) && (odd * (int64_t)es) % 16 == 0;
-    a.part[i] = {x.p, major[i], x.batch, x.head, x.row, n[i], width[i], i < 2 ? r : 0};
+    a.part[i] = {x.p, major[i], x.batch, x.head, x.row, n[i], width[i], i < 2 ? r : 0, 0, 0};
   }
   const Span pos = {positions, kind == LA2_POSITIONS_START   ? (size_t)B * 8
                                : kind == LA2_POSITIONS_TABLE ? (size_t)B * L * 8
@@ -1000,19 +1011,22 @@ la2_status rotary_call(const la2_heads *q, const la2_heads *k, const la2_heads *
   using namespace la2::rot;
   const int64_t tiles = (a.rows + TOK - 1) / TOK;
   if (tiles > INT32_MAX) return LA2_ERR_UNSUPPORTED;
-  // few tokens (decode): the heads of a token are spread over several CTAs
+  for (int i = 0; i < parts; i++) {
+    la2::rot::Part &q = a.part[i];
+    while (2 * (vec ? 8 : 1) << q.lanes < q.width) q.lanes++;
+    // fewer heads than groups of lanes: several groups to a head's sum
+    const int groups = LANES >> q.lanes, copies = i ? a.rep : 1;
+    while ((q.n << (q.split + 1)) <= groups && (2 << q.split) <= copies) q.split++;
+  }
+  // few tokens (decode): the tensors and heads of a token are spread over
+  // several CTAs
   const int per = LANES / (d / (vec ? 16 : 2));
   const int64_t groups = (H + per - 1) / per, want = (4 * (int64_t)device_sms() + tiles - 1) / tiles;
-  const dim3 grid((unsigned)tiles, (unsigned)(want < groups ? want : groups));
-  const size_t smem = (size_t)TOK * (r / 2) * sizeof(float2);
+  const dim3 grid((unsigned)tiles, (unsigned)(want < groups ? want : groups), want > 1 ? (unsigned)parts : 1u);
   const bool inter = (flags & LA2_ROTARY_INTERLEAVED) != 0;
   return to_status(timed(GRAD ? K_ROTARY_GRAD : K_ROTARY, stream, [&] {
-    if (dt == LA2_F32)
-      inter ? rotary_launch<float, GRAD, true>(a, grid, smem, vec, stream)
-            : rotary_launch<float, GRAD, false>(a, grid, smem, vec, stream);
-    else
-      inter ? rotary_launch<__nv_bfloat16, GRAD, true>(a, grid, smem, vec, stream)
-            : rotary_launch<__nv_bfloat16, GRAD, false>(a, grid, smem, vec, stream);
+    if (dt == LA2_F32) rotary_form<float, GRAD>(a, inter, grid, vec, stream);
+    else rotary_form<__nv_bfloat16, GRAD>(a, inter, grid, vec, stream);
   }));
 }
 

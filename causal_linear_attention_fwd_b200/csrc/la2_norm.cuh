@@ -61,9 +61,10 @@ template <typename T> struct Raw {
 #pragma unroll
     for (int i = 0; i < N; i++) r[i] = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void load(const T *p) {
+  // apart: values from one 16-byte piece to the next (fp32: 4 = neighbours)
+  __device__ __forceinline__ void load(const T *p, int apart = 4) {
 #pragma unroll
-    for (int i = 0; i < N; i++) r[i] = fmap::ld_stream(reinterpret_cast<const uint4 *>(p) + i);
+    for (int i = 0; i < N; i++) r[i] = fmap::ld_stream(p + i * apart);
   }
   __device__ __forceinline__ void load_shared(const T *p) {
 #pragma unroll

@@ -33,13 +33,13 @@ constexpr int LANES = NT / TOK;
 template <typename T, int V> struct Unit : norm::Raw<T> {};
 template <typename T> struct Unit<T, 1> {
   T r;
-  __device__ __forceinline__ void load(const T *p) { r = *p; }
+  __device__ __forceinline__ void load(const T *p, int) { r = *p; }
   __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = io<T>::ld(&r); }
 };
 template <typename T, int V>
-__device__ __forceinline__ void put(T *p, const float (&f)[V]) {
+__device__ __forceinline__ void put(T *p, const float (&f)[V], int apart) {
   if constexpr (V == 1) io<T>::st(p, f[0]);
-  else norm::store8(p, f);
+  else norm::store8(p, f, apart);
 }
 
 // One tensor: `n` heads of `width` columns on the strided side (strides in
@@ -49,6 +49,8 @@ struct Part {
   void *major;         // [B, n * rep, L, width] contiguous
   int64_t sb, sh, sl;
   int n, width, turn;  // turn: columns that are rotated (r, or 0 for v)
+  int lanes, split;    // log2 of the lanes of a head, of the groups of lanes
+                       // that share a head's sum
 };
 struct Args {
   Part part[3];
@@ -61,12 +63,16 @@ struct Args {
   float scale;
 };
 
-// V = 8: a lane moves 2 x 8 columns of one head (both members of 8 pairs);
-// V = 1: 2 columns, for widths, alignments or strides that 16-byte pieces do
-// not fit.  U heads' loads are issued before any of them is turned, and the
-// first ones before the table is made.
-template <typename T, bool GRAD, bool INTER, int V, int U>
-__global__ void __launch_bounds__(NT, 3) rotary_kernel(const __grid_constant__ Args a) {
+// V = 8: a lane moves 2 x 8 columns of one head, both members of 8 pairs; V =
+// 1: 2 columns, for widths, alignments or strides that 16-byte pieces do not
+// fit.  The lanes of a head share its turned columns and then the rest: lane c
+// of n takes 8 from 8 c on in each half of them (fp32: 4 from 4 c on and 4 n
+// further, in each half), so that every load and store of the lanes is one run
+// of bytes (a 32-byte stride between lanes moves every sector twice).  U heads'
+// loads are issued before any of them is turned, and the first ones before the
+// table is made.  SUMS: the backward where heads are shared.
+template <typename T, bool GRAD, bool SUMS, bool INTER, int V, int U>
+__global__ void __launch_bounds__(NT, SUMS ? 2 : 3) rotary_kernel(const __grid_constant__ Args a) {
   extern __shared__ float2 table[];  // [TOK][r / 2]
   const int64_t row0 = (int64_t)blockIdx.x * TOK;
   const int half = a.r / 2;
@@ -76,20 +82,24 @@ __global__ void __launch_bounds__(NT, 3) rotary_kernel(const __grid_constant__ A
   int64_t b = 0, t = 0;
   if (live) norm::split_row(row, a.L, b, t);
 #pragma unroll 1
-  for (int q = 0; q < a.parts; q++) {
+  for (int q = blockIdx.z; q < a.parts; q += gridDim.z) {
     const Part &p = a.part[q];
     const int rep = q == 0 ? 1 : a.rep;
-    const int chunks = p.width / (2 * V);      // lanes of one head
-    const int per = LANES / chunks;            // heads at a time
-    const int c = lane % chunks;
-    // the lane's columns: x0 from c0, x1 from c1
+    const int per = LANES >> p.lanes;          // heads at a time
+    const int c = lane & ((1 << p.lanes) - 1);
     const bool turned = c * 2 * V < p.turn;
-    const int c0 = turned && !INTER ? c * V : c * 2 * V;
-    const int c1 = turned && !INTER ? c0 + half : c0 + V;
+    const int n_lanes = (turned ? p.turn : p.width - p.turn) / (2 * V);
+    const int cc = turned ? c : c - p.turn / (2 * V);
+    // the lane's columns: x0 from c0, x1 from c1; apart: between fp32's pieces
+    constexpr int W = V == 8 && sizeof(T) == 4 ? 4 : V;
+    const int apart = n_lanes * 4;
+    const bool neighbours = V == 1 && INTER && turned;
+    const int c0 = neighbours ? 2 * cc : (turned ? 0 : p.turn) + cc * W;
+    const int c1 = neighbours ? c0 + 1 : c0 + n_lanes * V;
     const int64_t hstep = a.L * p.width;
     T *strided = static_cast<T *>(p.strided) + b * p.sb + t * p.sl;
     T *major = static_cast<T *>(p.major) + (b * p.n * rep * a.L + t) * p.width;
-    const int h0 = blockIdx.y * per + lane / chunks, stride = gridDim.y * per;
+    const int h0 = blockIdx.y * per + (lane >> p.lanes), stride = gridDim.y * per;
     const int n = live ? p.n : 0;
     Unit<T, V> x0[U], x1[U];
     auto fetch = [&](int h) {
@@ -98,35 +108,41 @@ __global__ void __launch_bounds__(NT, 3) rotary_kernel(const __grid_constant__ A
         const int hu = h + u * stride;
         if (hu < n) {
           const T *s = GRAD ? major + (int64_t)hu * hstep : strided + hu * p.sh;
-          x0[u].load(s + c0);
-          x1[u].load(s + c1);
+          x0[u].load(s + c0, apart);
+          x1[u].load(s + c1, apart);
         }
       }
     };
-    const bool sums = GRAD && rep > 1;  // a head's gradients come from several
+    const bool sums = SUMS && q > 0;  // a head's gradients come from several
     if (!sums) fetch(h0);
-    if (q == 0) {
+    if (q == (int)blockIdx.z && p.turn) {
+      const int64_t pos = !live ? 0 : a.pos_mode == 0 ? t : a.pos_mode == 1 ? a.pos[b] + t : a.pos[row];
 #pragma unroll 1
-      for (int i = threadIdx.x; i < TOK * half; i += NT) {
-        const int64_t r = row0 + i / half;
-        if (r >= a.rows) break;
-        int64_t rb, rt;
-        norm::split_row(r, a.L, rb, rt);
-        const int64_t pos = a.pos_mode == 0 ? rt : a.pos_mode == 1 ? a.pos[rb] + rt : a.pos[r];
+      for (int i = lane; i < half; i += LANES) {
         // the angle less its whole turns, in fp64; what is left fits fp32
-        const double turns = (double)pos * a.freq[i % half] * 0.15915494309189533577;
+        const double turns = (double)pos * a.freq[i] * 0.15915494309189533577;
         float sn, cs;
         sincospif(2.f * (float)(turns - rint(turns)), &sn, &cs);
-        table[i] = make_float2(cs * a.scale, (GRAD ? -sn : sn) * a.scale);
+        table[sub * half + i] = make_float2(cs * a.scale, (GRAD ? -sn : sn) * a.scale);
       }
       __syncthreads();
     }
-    float2 w[V];
-    if (turned && live) {
+    // the pairs of x0's values (and x1's, which are the same ones); pairs of
+    // neighbours: x0's four, then x1's four
+    auto angles = [&](float2 (&w)[V]) {
 #pragma unroll
-      for (int i = 0; i < V; i++) w[i] = table[sub * half + c * V + i];
-    }
-    auto turn = [&](float (&f)[V], float (&g)[V]) {
+      for (int i = 0; i < V; i++) {
+        int pr;
+        if (V == 8 && INTER) {
+          const int k = i % 4;
+          pr = (W == 4 ? k / 2 * n_lanes * 2 + cc * 2 + k % 2 : cc * 4 + k) + i / 4 * n_lanes * 4;
+        } else {
+          pr = W == 4 ? i / 4 * apart + cc * 4 + i % 4 : cc * V + i;
+        }
+        if (turned) w[i] = table[sub * half + pr];
+      }
+    };
+    auto turn = [&](float (&f)[V], float (&g)[V], const float2 (&w)[V]) {
       if (!turned) return;
       if (V > 1 && INTER) {
         // pairs are neighbours: f holds the first V / 2 pairs, g the rest
@@ -149,6 +165,8 @@ __global__ void __launch_bounds__(NT, 3) rotary_kernel(const __grid_constant__ A
       }
     };
     if (!sums) {
+      float2 w[V];
+      angles(w);
       for (int h = h0; h < n; h += U * stride) {
         if (h != h0) fetch(h);
 #pragma unroll
@@ -158,37 +176,44 @@ __global__ void __launch_bounds__(NT, 3) rotary_kernel(const __grid_constant__ A
           float f[V], g[V];
           x0[u].get(f);
           x1[u].get(g);
-          turn(f, g);
+          turn(f, g, w);
           if constexpr (GRAD) {
-            put<T, V>(strided + hu * p.sh + c0, f);
-            put<T, V>(strided + hu * p.sh + c1, g);
+            put<T, V>(strided + hu * p.sh + c0, f, apart);
+            put<T, V>(strided + hu * p.sh + c1, g, apart);
           } else {
             T *m = major + (int64_t)hu * rep * hstep;
 #pragma unroll 1
             for (int j = 0; j < rep; j++, m += hstep) {
-              put<T, V>(m + c0, f);
-              put<T, V>(m + c1, g);
+              put<T, V>(m + c0, f, apart);
+              put<T, V>(m + c1, g, apart);
             }
           }
         }
       }
-    } else {
-      for (int h = h0; h < n; h += stride) {
+    } else if constexpr (SUMS) {
+      // `split` groups of lanes share a head's copies where there are fewer
+      // heads than groups; their partial sums meet in shared memory
+      float *partial = reinterpret_cast<float *>(table + TOK * half);  // [2 V][NT]
+      const int split = 1 << p.split, heads = per >> p.split, group = lane >> p.lanes;
+      const int s = group & (split - 1), begin = s * rep >> p.split;
+      for (int hb = blockIdx.y * heads; hb < p.n; hb += gridDim.y * heads) {
+        const int h = hb + (group >> p.split);
         const T *m = major + (int64_t)h * rep * hstep;
+        const int end = h < n ? (s + 1) * rep >> p.split : 0;
         float f[V], g[V];
 #pragma unroll
         for (int i = 0; i < V; i++) f[i] = g[i] = 0.f;
-        for (int j = 0; j < rep; j += U) {
+        for (int j = begin; j < end; j += U) {
 #pragma unroll
           for (int u = 0; u < U; u++) {
-            if (j + u < rep) {
-              x0[u].load(m + (j + u) * hstep + c0);
-              x1[u].load(m + (j + u) * hstep + c1);
+            if (j + u < end) {
+              x0[u].load(m + (j + u) * hstep + c0, apart);
+              x1[u].load(m + (j + u) * hstep + c1, apart);
             }
           }
 #pragma unroll
           for (int u = 0; u < U; u++) {
-            if (j + u < rep) {
+            if (j + u < end) {
               float y0[V], y1[V];
               x0[u].get(y0);
               x1[u].get(y1);
@@ -200,9 +225,31 @@ __global__ void __launch_bounds__(NT, 3) rotary_kernel(const __grid_constant__ A
             }
           }
         }
-        turn(f, g);
-        put<T, V>(strided + h * p.sh + c0, f);
-        put<T, V>(strided + h * p.sh + c1, g);
+        if (split > 1) {
+          __syncthreads();  // the last round's are read
+          if (s) {
+#pragma unroll
+            for (int i = 0; i < V; i++) {
+              partial[i * NT + threadIdx.x] = f[i];
+              partial[(V + i) * NT + threadIdx.x] = g[i];
+            }
+          }
+          __syncthreads();
+          if (s) continue;
+          for (int k = 1; k < split; k++) {
+#pragma unroll
+            for (int i = 0; i < V; i++) {
+              f[i] += partial[i * NT + threadIdx.x + (k << p.lanes)];
+              g[i] += partial[(V + i) * NT + threadIdx.x + (k << p.lanes)];
+            }
+          }
+        }
+        if (h >= n) continue;
+        float2 w[V];  // not held while the sums are made
+        angles(w);
+        turn(f, g, w);
+        put<T, V>(strided + h * p.sh + c0, f, apart);
+        put<T, V>(strided + h * p.sh + c1, g, apart);
       }
     }
   }
