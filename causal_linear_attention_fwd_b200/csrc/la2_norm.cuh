@@ -42,6 +42,7 @@
 
 #include <type_traits>
 
+#include "la2_bulk.cuh"
 #include "la2_common.cuh"
 #include "la2_fmap.cuh"
 #include "la2_sm100.cuh"
@@ -323,7 +324,7 @@ struct RowSum {
 #pragma unroll
           for (int k = 0; k < K; k++) send(smem_u32(&s.red[turn][k][rank * NW + w]), bar, l, x[k]);
         }
-        mbar_wait(bar, (uses >> 1) & 1, abort);
+        bulk::wait(bar, (uses >> 1) & 1, abort);
         if (threadIdx.x == 0) mbar_expect_tx(bar, (uint32_t)(cl * NW * K * sizeof(float)));
 #pragma unroll
         for (int k = 0; k < K; k++) {
@@ -698,13 +699,6 @@ struct Residual {
 // sums, stay the same.
 constexpr int kRingHead = 128;  // barriers, in front of the ring
 
-__device__ __forceinline__ void bulk_row(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
 // The values of one row that a thread holds: forward h, y; backward h', dn,
 // dh', y (dh' and y where they are).
 template <typename T, typename R, bool GRAD, bool POST, int NV>
@@ -803,7 +797,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) residual_kernel(const _
       n = (int)(total - at) / PIECE * PIECE;
       for (int i = n; i < hi; i++) reinterpret_cast<X *>(to)[i] = x[at + i];
     }
-    if (!ODD || n) bulk_row(smem_u32(to), x + at, (uint32_t)(n * sizeof(X)), bar);
+    if (!ODD || n) bulk::load(smem_u32(to), x + at, (uint32_t)(n * sizeof(X)), bar);
     return (uint32_t)(n * sizeof(X));
   };
   auto fetch = [&](int64_t row, int st) {  // thread 0
@@ -876,7 +870,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) residual_kernel(const _
     const char *stage = ring + st * stage_bytes;
     // on a timeout the values are stale, but every thread stays in step with
     // the barriers below; the error word tells the host
-    if constexpr (RING) mbar_wait(bars + st * 8, (uint32_t)(it >> shift) & 1, abort);
+    if constexpr (RING) bulk::wait(bars + st * 8, (uint32_t)(it >> shift) & 1, abort);
 #pragma unroll
     for (int n = 0; n < NV; n++) {
       const int c = col(n);
@@ -1064,7 +1058,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) residual_kernel(const _
     if (threadIdx.x == 0 && *abort) {
       volatile int none = 0;
       for (int64_t j = it > p.stages ? it - p.stages : 0; j < it; j++)
-        mbar_wait(bars + ((uint32_t)j & shift) * 8, (uint32_t)(j >> shift) & 1, &none);
+        bulk::wait(bars + ((uint32_t)j & shift) * 8, (uint32_t)(j >> shift) & 1, &none);
     }
   }
   if constexpr (GRAD) {

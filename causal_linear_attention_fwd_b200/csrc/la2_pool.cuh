@@ -18,8 +18,8 @@
 // is refilled by the very thread whose stores read it.
 #pragma once
 
+#include "la2_bulk.cuh"
 #include "la2_common.cuh"
-#include "la2_sm100.cuh"
 
 namespace la2 {
 namespace pool {
@@ -28,30 +28,12 @@ using namespace sm100;
 
 constexpr int NT = 256;
 constexpr int MAX_MOVES = 4096;
-constexpr int MAX_W = 8192;       // widest slab
+constexpr int MAX_W = 4096;       // widest slab
 constexpr int MAX_STAGES = 8;
 constexpr int SMEM = 227 * 1024;  // what a CTA may have
 constexpr int HEAD = 256;         // barriers, counters
 // shared memory: HEAD, then MAX_W zero bytes, the list of moves, the ring
 constexpr int ring_bytes(int n) { return (SMEM - HEAD - MAX_W - (n * 8 + 127) / 128 * 128) / 128 * 128; }
-
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                   reinterpret_cast<uint64_t>(dst)),
-               "r"(src), "r"(bytes)
-               : "memory");
-}
-// all but this thread's newest group of bulk stores have read their source
-__device__ __forceinline__ void bulk_wait_read1() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
 
 // from [layers, from_size, bytes], to [layers, to_size, bytes]; `bytes` a
 // multiple of 16.
@@ -88,12 +70,15 @@ copy_kernel(const char *from, char *to, const int *src, const int *dst, int n, i
   const int m = *count;
   if (m == 0) return;
 
-  // The slab's width: three slabs of all moves in the ring (two where that
-  // would leave less than 512 bytes of each state), and no wider than gives
-  // every CTA a slab.
+  // The slab's width: four slabs of all moves in the ring, or three or two
+  // where that would leave less than 768 or 256 bytes of each state, and no
+  // wider than gives every CTA a slab.  (Narrow pieces cost: 200 moves of
+  // 4 MiB took 512 us at 128 bytes each, 313 with two slabs of 512, 274 with
+  // three of 256.)
   const int room = ring_bytes(n);
-  int w = room / 3 / m;
-  if (w < 512) w = room / 2 / m;
+  int w = room / 4 / m;
+  if (w < 768) w = room / 3 / m;
+  if (w < 256) w = room / 2 / m;
   const int64_t share = (bytes * layers + gridDim.x - 1) / gridDim.x;
   if (w > share) w = (int)share;
   if (w > MAX_W) w = MAX_W;
@@ -110,55 +95,71 @@ copy_kernel(const char *from, char *to, const int *src, const int *dst, int n, i
   __syncthreads();
   if (tid >= users) return;
 
-  const int64_t slabs_row = (bytes + w - 1) / w, slabs = slabs_row * layers;
-  const int64_t mine = (slabs - blockIdx.x + gridDim.x - 1) / gridDim.x;  // this CTA's slabs
-  auto place = [&](int64_t it, int64_t &layer, int64_t &off, uint32_t &len) {
-    const int64_t s = blockIdx.x + it * gridDim.x;
-    layer = s / slabs_row;
-    off = (s - layer * slabs_row) * w;
-    len = (uint32_t)(bytes - off < w ? bytes - off : w);
+  // Slab s of layer l is bytes [s w, s w + w) of every state of that layer;
+  // this CTA's are gridDim.x apart, counted through the layers.
+  const int slabs_row = (int)((bytes + w - 1) / w);
+  struct Place {
+    int slab, layer, stage;
   };
-  auto load = [&](int64_t it) {
-    int64_t layer, off;
-    uint32_t len, total = 0;
-    place(it, layer, off, len);
-    const int st = (int)(it % stages);
+  auto next = [&](Place &p) {
+    p.slab += gridDim.x;
+    while (p.slab >= slabs_row && p.layer < layers) {
+      p.slab -= slabs_row;
+      p.layer++;
+    }
+    if (++p.stage == stages) p.stage = 0;
+  };
+  auto length = [&](const Place &p) {
+    const int64_t left = bytes - (int64_t)p.slab * w;
+    return (uint32_t)(left < w ? left : w);
+  };
+  auto load = [&](const Place &p) {
+    const uint32_t len = length(p), bar = smem_u32(bars + p.stage);
+    const char *base = from + (int64_t)p.layer * from_size * bytes + (int64_t)p.slab * w;
+    uint32_t total = 0;
     for (int i = tid; i < m; i += NT) total += list[i].x >= 0 ? len : 0;
-    mbar_expect_tx(smem_u32(bars + st), total);
+    mbar_expect_tx(bar, total);
     for (int i = tid; i < m; i += NT) {
       const int s = list[i].x;
-      if (s >= 0)
-        bulk_load(smem_u32(ring + ((int64_t)st * m + i) * w),
-                  from + (layer * from_size + s) * bytes + off, len, smem_u32(bars + st));
+      if (s >= 0) bulk::load(smem_u32(ring) + (uint32_t)(p.stage * m + i) * w, base + s * bytes, len, bar);
     }
   };
-  const int ahead = stages - 1;
-  for (int64_t it = 0; it < ahead && it < mine; it++) load(it);
-  int64_t it = 0;
+  Place at{(int)blockIdx.x, 0, 0}, ahead;
+  at.slab -= gridDim.x;
+  at.stage = -1;
+  next(at);
+  ahead = at;
+  for (int i = 0; i < stages && ahead.layer < layers; i++, next(ahead)) load(ahead);
   bool ok = true;
-  for (; it < mine; it++) {
-    if (it + ahead < mine && it == 0) load(ahead);  // the one buffer not yet used
-    const int st = (int)(it % stages);
-    ok = mbar_wait(smem_u32(bars + st), (uint32_t)(it / stages) & 1, abort);
+  uint32_t phase = 0;
+  for (int it = 0; at.layer < layers; it++) {
+    ok = bulk::wait(smem_u32(bars + at.stage), phase, abort);
     if (!ok) break;
-    int64_t layer, off;
-    uint32_t len;
-    place(it, layer, off, len);
+    const uint32_t len = length(at);
+    char *base = to + (int64_t)at.layer * to_size * bytes + (int64_t)at.slab * w;
     for (int i = tid; i < m; i += NT)
-      bulk_store(to + (layer * to_size + list[i].y) * bytes + off,
-                 list[i].x >= 0 ? smem_u32(ring + ((int64_t)st * m + i) * w) : smem_u32(zeros), len);
+      bulk::store(base + list[i].y * bytes,
+                 list[i].x >= 0 ? smem_u32(ring) + (uint32_t)(at.stage * m + i) * w : smem_u32(zeros), len);
     tma_store_commit();
+    next(at);
+    if (at.stage == 0) phase ^= 1;
     // refill the slab before this one, whose stores are an iteration old
-    if (it >= 1 && it + ahead < mine) {
-      bulk_wait_read1();
-      load(it + ahead);
+    // (waiting for older ones instead leaves fewer slabs on their way: 200
+    // moves 287 us against 274)
+    if (it >= 1 && ahead.layer < layers) {
+      bulk::wait_read1();
+      load(ahead);
+      next(ahead);
     }
   }
   if (!ok) {
     // gave up: let this CTA's own loads land before its memory is released
     volatile int none = 0;
-    for (int64_t j = it; j <= it + ahead && j < mine; j++)
-      mbar_wait(smem_u32(bars + j % stages), (uint32_t)(j / stages) & 1, &none);
+    for (; at.stage != ahead.stage || at.slab != ahead.slab || at.layer != ahead.layer;) {
+      bulk::wait(smem_u32(bars + at.stage), phase, &none);
+      next(at);
+      if (at.stage == 0) phase ^= 1;
+    }
   }
   tma_store_wait0();
 }
