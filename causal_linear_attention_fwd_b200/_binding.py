@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import json
 import math
 import os
@@ -647,6 +648,12 @@ def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_floats(op, B, H, L, d, e, dt, device_index):
+    """Size of a norm backward's workspace: it depends on these alone."""
+    return int(library().la2_workspace_size(op, B, H, L, d, e, dt)) // 4
+
+
 def _row_strides(name, t):
     """A [B,L,columns] tensor's strides of batch and row."""
     st = t.stride()
@@ -748,8 +755,9 @@ def rotary(q, k, inv_freq, positions=None, *, v=None, interleaved: bool = False,
     r, kind = _rotary_args(inv_freq, positions, B, L, dev)
     with _guard(dev):
         if out is None:
-            rq, rk = q.new_empty(shape), q.new_empty(shape)
-            rv = None if v is None else q.new_empty((B, H, L, e))
+            rq = q.new_empty(shape)
+            rk = torch.empty_like(rq)
+            rv = None if v is None else torch.empty_like(rq) if e == d else q.new_empty((B, H, L, e))
         else:
             if len(out) != (2 if v is None else 3):
                 raise ValueError(f"out must be {2 if v is None else 3} buffers")
@@ -886,8 +894,8 @@ def gated_norm_backward(du, o, gate=None, weight=None, *, activation: str = "sil
             dgate = None if gate is None else o.new_empty((B, L, H * e))
         dw = None if weight is None else torch.empty_like(weight)
         if workspace is None and dw is not None:
-            workspace = _workspace(
-                workspace_size(LA2_OP_GATED_NORM_BACKWARD, B, H, L, e, e, dtype), dev)
+            workspace = dw.new_empty(_norm_floats(LA2_OP_GATED_NORM_BACKWARD, B, H, L, e, e,
+                                                  _dt(o), dev.index))
         sb, sl = (0, 0) if gate is None else _row_strides("gate", gate)
         tb, tl = (0, 0) if gate is None else _row_strides("dgate", dgate)
         code = lib.la2_gated_norm_backward(du.data_ptr(), o.data_ptr(), _at(gate), sb, sl,
@@ -984,8 +992,8 @@ def residual_norm_backward(dn, h_new, y=None, weight=None, *, dh_new=None, post_
         dw = None if weight is None else torch.empty_like(weight)
         dpw = None if post_weight is None else torch.empty_like(post_weight)
         if workspace is None and (dw is not None or dpw is not None):
-            workspace = _workspace(
-                workspace_size(LA2_OP_RESIDUAL_NORM_BACKWARD, 1, 1, N, D, D, dn.dtype), dev)
+            workspace = (dpw if dw is None else dw).new_empty(
+                _norm_floats(LA2_OP_RESIDUAL_NORM_BACKWARD, 1, 1, N, D, D, _dt(dn), dev.index))
         code = lib.la2_residual_norm_backward(
             dn.data_ptr(), _at(dh_new), h_new.data_ptr(), _dt(h_new), _at(y), _at(weight),
             _at(post_weight), dh.data_ptr(), _at(dy), _at(dw), _at(dpw), alpha, beta, eps, flags,

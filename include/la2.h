@@ -336,7 +336,7 @@ la2_status la2_feature_map_backward(const void *q, const void *k, const void *dp
  * la2_rotary_backward: the chain rule.  dq, dk [B,H,L,d], dv [B,H,L,e]
  * (contiguous, as la2_backward writes them) to gq, gk, gv of q's, k's and v's
  * shapes, written through their strides: the copies of a shared head are added
- * (fp32, in the order of the heads), pairs turn by the opposite angle times
+ * (fp32, in a fixed order), pairs turn by the opposite angle times
  * scale.  gq, gk and gv may be slices of one buffer (side by side in each row
  * or each head); otherwise no two values may share a place.
  *
