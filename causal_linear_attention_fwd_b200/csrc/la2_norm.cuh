@@ -253,6 +253,34 @@ __device__ __forceinline__ void lanes_sum(float (&x)[K]) {
     for (int k = 0; k < K; k++) x[k] += __shfl_xor_sync(0xffffffffu, x[k], m);
   }
 }
+// Sums of K (5 to 8) values over a warp, one to every four lanes: lanes 4 k to
+// 4 k + 3 get value k's.  Each of the first three steps hands half of the
+// values over, so it takes 9 shuffles instead of 5 K.
+template <int K>
+__device__ __forceinline__ float warp_sums(const float (&x)[K]) {
+  const int lane = threadIdx.x % 32;
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; k++) v[k] = k < K ? x[k] : 0.f;
+#pragma unroll
+  for (int half = 4; half > 0; half /= 2) {
+    const bool upper = lane & (4 * half);
+#pragma unroll
+    for (int i = 0; i < half; i++) {
+      const float give = upper ? v[i] : v[i + half], keep = upper ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * half);
+    }
+  }
+  float y[1] = {v[0]};
+  lanes_sum<1, 4>(y);
+  return y[0];
+}
+// and back: every lane gets all K
+template <int K>
+__device__ __forceinline__ void spread(float (&x)[K], float y) {
+#pragma unroll
+  for (int k = 0; k < K; k++) x[k] = __shfl_sync(0xffffffffu, y, 4 * k);
+}
 __device__ __forceinline__ void cluster_arrive_wait() {
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
@@ -281,11 +309,15 @@ __device__ __forceinline__ void send(uint32_t to, uint32_t bar, uint32_t rank, f
 // between, to which every warp contributes only after reading this one.
 // Within a cluster the values are counted by an mbarrier of the receiving
 // CTA: a barrier of the whole cluster would also wait for the row's stores
-// (measured at 16,384 rows of 8,192 columns: 487 us, against the time above
-// the plan in la2_api.cu).  A wait that gives up leaves a stale sum; the
+// (16,384 columns in fp32 by clusters of two, forward: 430 us so, 358 by
+// counting).  A wait that gives up leaves a stale sum; the
 // caller's loop runs on, so that no barrier is missed, and the error word
 // tells the host.
-template <int TPR, int K, int MAXCL>
+// HAND_OVER: the form for many values that issues fewer instructions but waits
+// longer for each (residual norm's backward: 3 to 5 % faster where a row is
+// held by one unit a thread or by 512 threads, 4 % slower with two units and
+// 256).
+template <int TPR, int K, int MAXCL, bool HAND_OVER = false>
 struct RowSum {
   static constexpr int NW = TPR / 32;
   struct Shared {
@@ -306,6 +338,31 @@ struct RowSum {
   }
   __device__ __forceinline__ void operator()(float (&x)[K], Shared &s, int cl, int rank,
                                              volatile int *abort) {
+    if constexpr (HAND_OVER) {
+      float y = warp_sums(x);
+      if constexpr (TPR > 32) {
+        const int w = threadIdx.x / 32, l = threadIdx.x % 32, turn = uses & 1, k = l / 4, j = l % 4;
+        if (cl == 1) {
+          if (j == 0 && k < K) s.red[turn][k][w] = y;
+          __syncthreads();
+        } else {
+          const uint32_t bar = smem_u32(&s.bars[turn]);
+          // lane j of value k's four sends it to CTAs j and j + 4
+          for (int to = j; to < cl; to += 4)
+            if (k < K) send(smem_u32(&s.red[turn][k][rank * NW + w]), bar, to, y);
+          bulk::wait(bar, (uses >> 1) & 1, abort);
+          if (threadIdx.x == 0) mbar_expect_tx(bar, (uint32_t)(cl * NW * K * sizeof(float)));
+        }
+        float z[1] = {0.f};
+        if (k < K)
+          for (int i = j; i < cl * NW; i += 4) z[0] += s.red[turn][k][i];
+        lanes_sum<1, 4>(z);
+        y = z[0];
+        uses++;
+      }
+      spread(x, y);
+      return;
+    }
     lanes_sum<K, 32>(x);
     if constexpr (TPR > 32) {
       const int w = threadIdx.x / 32, l = threadIdx.x % 32, turn = uses & 1;
@@ -714,7 +771,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) residual_kernel(const _
   constexpr bool HAS_Y = !GRAD || POST;  // y may be read
   constexpr int RPC = NT / TPR, P = 4;
   // 16,384 columns take four CTAs, the up to 7 places more of odd rows eight
-  using Sum = RowSum<TPR, !GRAD ? 1 : POST ? 6 : 2, ODD ? 8 : 4>;
+  using Sum = RowSum<TPR, !GRAD ? 1 : POST ? 6 : 2, ODD ? 8 : 4, GRAD && POST && (NV == 1 || NT == 512)>;
   __shared__ typename Sum::Shared red;
   extern __shared__ __align__(128) char dyn[];
   Sum sum;
