@@ -931,22 +931,28 @@ bool apart(const la2_heads &x, int nx, int wx, const la2_heads &y, int ny, int w
   return side_by_side(wx, wy, {{x.batch, B}, {x.row, L}, {nx > 1 ? x.head : y.head, n}});
 }
 
-template <typename T, bool GRAD, bool SUMS, bool INTER>
-void rotary_launch(const la2::rot::Args &a, dim3 grid, bool vec, cudaStream_t st) {
+template <typename T, bool GRAD, bool SUMS, bool INTER, int V, int U>
+cudaError_t rotary_launch(const la2::rot::Args &a, dim3 grid, cudaStream_t st) {
   using namespace la2::rot;
-  const size_t smem = (size_t)TOK * (a.r / 2) * sizeof(float2) + (SUMS ? NT * 2 * (vec ? 8 : 1) * sizeof(float) : 0);
-  if (vec) rotary_kernel<T, GRAD, SUMS, INTER, 8, sizeof(T) == 2 ? 4 : 2><<<grid, NT, smem, st>>>(a);
-  else rotary_kernel<T, GRAD, SUMS, INTER, 1, 4><<<grid, NT, smem, st>>>(a);
+  auto kern = rotary_kernel<T, GRAD, SUMS, INTER, V, U>;
+  const size_t smem = (size_t)TOK * (a.r / 2) * sizeof(float2) + (SUMS ? sums_smem<T, V>() : 0);
+  if (smem > 32 * 1024)
+    if (cudaError_t e = opt_in_smem(kern, smem)) return e;
+  kern<<<grid, NT, smem, st>>>(a);
+  return cudaSuccess;
+}
+template <typename T, bool GRAD, bool SUMS, bool INTER>
+cudaError_t rotary_vec(const la2::rot::Args &a, dim3 grid, bool vec, cudaStream_t st) {
+  return vec ? rotary_launch<T, GRAD, SUMS, INTER, 8, sizeof(T) == 2 ? 4 : 2>(a, grid, st)
+             : rotary_launch<T, GRAD, SUMS, INTER, 1, 4>(a, grid, st);
 }
 template <typename T, bool GRAD>
-void rotary_form(const la2::rot::Args &a, bool inter, dim3 grid, bool vec, cudaStream_t st) {
-  if (GRAD && a.rep > 1) {
-    inter ? rotary_launch<T, GRAD, GRAD, true>(a, grid, vec, st)
-          : rotary_launch<T, GRAD, GRAD, false>(a, grid, vec, st);
-  } else {
-    inter ? rotary_launch<T, GRAD, false, true>(a, grid, vec, st)
-          : rotary_launch<T, GRAD, false, false>(a, grid, vec, st);
-  }
+cudaError_t rotary_form(const la2::rot::Args &a, bool inter, dim3 grid, bool vec, cudaStream_t st) {
+  if (GRAD && a.rep > 1)
+    return inter ? rotary_vec<T, GRAD, GRAD, true>(a, grid, vec, st)
+                 : rotary_vec<T, GRAD, GRAD, false>(a, grid, vec, st);
+  return inter ? rotary_vec<T, GRAD, false, true>(a, grid, vec, st)
+               : rotary_vec<T, GRAD, false, false>(a, grid, vec, st);
 }
 
 template <bool GRAD>
@@ -1025,8 +1031,8 @@ la2_status rotary_call(const la2_heads *q, const la2_heads *k, const la2_heads *
   const dim3 grid((unsigned)tiles, (unsigned)(want < groups ? want : groups), want > 1 ? (unsigned)parts : 1u);
   const bool inter = (flags & LA2_ROTARY_INTERLEAVED) != 0;
   return to_status(timed(GRAD ? K_ROTARY_GRAD : K_ROTARY, stream, [&] {
-    if (dt == LA2_F32) rotary_form<float, GRAD>(a, inter, grid, vec, stream);
-    else rotary_form<__nv_bfloat16, GRAD>(a, inter, grid, vec, stream);
+    return dt == LA2_F32 ? rotary_form<float, GRAD>(a, inter, grid, vec, stream)
+                         : rotary_form<__nv_bfloat16, GRAD>(a, inter, grid, vec, stream);
   }));
 }
 

@@ -63,6 +63,14 @@ struct Args {
   float scale;
 };
 
+// Copies of a shared head on their way per thread (128 bytes).
+template <typename T, int V>
+constexpr int sums_ahead() { return V == 8 ? 8 / (int)sizeof(T) : 0; }
+template <typename T, int V>
+constexpr size_t sums_smem() {
+  return NT * (2 * V * sizeof(float) + 2 * sums_ahead<T, V>() * 2 * V * sizeof(T));
+}
+
 // V = 8: a lane moves 2 x 8 columns of one head, both members of 8 pairs; V =
 // 1: 2 columns, for widths, alignments or strides that 16-byte pieces do not
 // fit.  The lanes of a head share its turned columns and then the rest: lane c
@@ -81,24 +89,70 @@ __global__ void __launch_bounds__(NT, SUMS ? 2 : 3) rotary_kernel(const __grid_c
   const bool live = row < a.rows;
   int64_t b = 0, t = 0;
   if (live) norm::split_row(row, a.L, b, t);
+  // where this lane's values of a tensor are
+  struct View {
+    int per, cc, n_lanes, c0, c1;
+    bool turned;
+    int64_t hstep;
+    T *strided, *major;
+  };
+  constexpr int W = V == 8 && sizeof(T) == 4 ? 4 : V;
+  auto view = [&](const Part &p, int rep) {
+    View w;
+    w.per = LANES >> p.lanes;  // heads at a time
+    const int c = lane & ((1 << p.lanes) - 1);
+    w.turned = c * 2 * V < p.turn;
+    w.n_lanes = (w.turned ? p.turn : p.width - p.turn) / (2 * V);
+    w.cc = w.turned ? c : c - p.turn / (2 * V);
+    // the lane's columns: x0 from c0, x1 from c1
+    const bool neighbours = V == 1 && INTER && w.turned;
+    w.c0 = neighbours ? 2 * w.cc : (w.turned ? 0 : p.turn) + w.cc * W;
+    w.c1 = neighbours ? w.c0 + 1 : w.c0 + w.n_lanes * V;
+    w.hstep = a.L * p.width;
+    w.strided = static_cast<T *>(p.strided) + b * p.sb + t * p.sl;
+    w.major = static_cast<T *>(p.major) + (b * p.n * rep * a.L + t) * p.width;
+    return w;
+  };
+  // SUMS: the first copies of the first heads of k and v are on their way into
+  // the thread's own places of shared memory while q is worked on.
+  constexpr int AHEAD = SUMS ? sums_ahead<T, V>() : 0, PIECES = 2 * sizeof(T) / 2;
+  float *partial = reinterpret_cast<float *>(table + TOK * half);  // [2 V][NT]
+  auto ahead = [&](int q, int copy, int piece) {
+    return reinterpret_cast<uint4 *>(partial + 2 * V * NT) +
+           (((q - 1) * AHEAD + copy) * PIECES + piece) * NT + threadIdx.x;
+  };
+  if constexpr (AHEAD > 0) {
+    for (int q = blockIdx.z; q < a.parts; q += gridDim.z) {
+      const Part &p = a.part[q];
+      const View w = view(p, a.rep);
+      const int group = lane >> p.lanes, s = group & ((1 << p.split) - 1);
+      const int h = blockIdx.y * (w.per >> p.split) + (group >> p.split);
+      if (q > 0 && live && h < p.n) {
+        const int begin = s * a.rep >> p.split, end = (s + 1) * a.rep >> p.split;
+        const T *m = w.major + (int64_t)(h * a.rep + begin) * w.hstep;
+#pragma unroll
+        for (int j = 0; j < AHEAD; j++, m += w.hstep)
+          if (begin + j < end) {
+#pragma unroll
+            for (int k = 0; k < PIECES / 2; k++) {
+              norm::copy16_async(ahead(q, j, k), m + w.c0 + k * w.n_lanes * 4);
+              norm::copy16_async(ahead(q, j, PIECES / 2 + k), m + w.c1 + k * w.n_lanes * 4);
+            }
+          }
+      }
+    }
+    norm::copies_commit();
+  }
 #pragma unroll 1
   for (int q = blockIdx.z; q < a.parts; q += gridDim.z) {
     const Part &p = a.part[q];
     const int rep = q == 0 ? 1 : a.rep;
-    const int per = LANES >> p.lanes;          // heads at a time
-    const int c = lane & ((1 << p.lanes) - 1);
-    const bool turned = c * 2 * V < p.turn;
-    const int n_lanes = (turned ? p.turn : p.width - p.turn) / (2 * V);
-    const int cc = turned ? c : c - p.turn / (2 * V);
-    // the lane's columns: x0 from c0, x1 from c1; apart: between fp32's pieces
-    constexpr int W = V == 8 && sizeof(T) == 4 ? 4 : V;
-    const int apart = n_lanes * 4;
-    const bool neighbours = V == 1 && INTER && turned;
-    const int c0 = neighbours ? 2 * cc : (turned ? 0 : p.turn) + cc * W;
-    const int c1 = neighbours ? c0 + 1 : c0 + n_lanes * V;
-    const int64_t hstep = a.L * p.width;
-    T *strided = static_cast<T *>(p.strided) + b * p.sb + t * p.sl;
-    T *major = static_cast<T *>(p.major) + (b * p.n * rep * a.L + t) * p.width;
+    const View at = view(p, rep);
+    const int per = at.per, cc = at.cc, n_lanes = at.n_lanes, c0 = at.c0, c1 = at.c1;
+    const int apart = n_lanes * 4;  // between fp32's pieces
+    const bool turned = at.turned;
+    const int64_t hstep = at.hstep;
+    T *strided = at.strided, *major = at.major;
     const int h0 = blockIdx.y * per + (lane >> p.lanes), stride = gridDim.y * per;
     const int n = live ? p.n : 0;
     Unit<T, V> x0[U], x1[U];
@@ -193,7 +247,6 @@ __global__ void __launch_bounds__(NT, SUMS ? 2 : 3) rotary_kernel(const __grid_c
     } else if constexpr (SUMS) {
       // `split` groups of lanes share a head's copies where there are fewer
       // heads than groups; their partial sums meet in shared memory
-      float *partial = reinterpret_cast<float *>(table + TOK * half);  // [2 V][NT]
       const int split = 1 << p.split, heads = per >> p.split, group = lane >> p.lanes;
       const int s = group & (split - 1), begin = s * rep >> p.split;
       for (int hb = blockIdx.y * heads; hb < p.n; hb += gridDim.y * heads) {
@@ -203,7 +256,32 @@ __global__ void __launch_bounds__(NT, SUMS ? 2 : 3) rotary_kernel(const __grid_c
         float f[V], g[V];
 #pragma unroll
         for (int i = 0; i < V; i++) f[i] = g[i] = 0.f;
-        for (int j = begin; j < end; j += U) {
+        int j = begin;
+        if constexpr (AHEAD > 0) {
+          if (hb == (int)blockIdx.y * heads) {
+            norm::copies_wait<0>();
+#pragma unroll
+            for (int u = 0; u < AHEAD; u++, j++) {
+              if (j < end) {
+                norm::Raw<T> r0, r1;
+#pragma unroll
+                for (int k = 0; k < PIECES / 2; k++) {
+                  r0.r[k] = *ahead(q, u, k);
+                  r1.r[k] = *ahead(q, u, PIECES / 2 + k);
+                }
+                float y0[8], y1[8];
+                r0.get(y0);
+                r1.get(y1);
+#pragma unroll
+                for (int i = 0; i < V; i++) {
+                  f[i] += y0[i];
+                  g[i] += y1[i];
+                }
+              }
+            }
+          }
+        }
+        for (; j < end; j += U) {
 #pragma unroll
           for (int u = 0; u < U; u++) {
             if (j + u < end) {
