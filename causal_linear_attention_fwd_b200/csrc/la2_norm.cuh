@@ -38,6 +38,20 @@
 // columns over all rows its CTA walks, so each CTA (or cluster) writes one row
 // of partial sums to the workspace, and colsum_kernel adds those rows in a
 // fixed order: no atomics, the same result on every run.
+//
+// Measured on B200 (bf16 unless named, cold L2, of the copy bandwidth):
+//   gated norm    65,536 x 4,096, one norm a row     271 us  (91 %)
+//                 8,192 x 8,192 per head, fp32       139 us  (89 %)
+//                 256 x 8,192, one token a request   9-10 us (the launch and
+//                                                    one trip to memory)
+//     backward    8,196 x 4,096 per head             66 us   (78 %: 39
+//                 instructions a value, issue slots 68 % busy)
+//   residual norm 65,536 x 4,096                     351 us  (94 %)
+//                 16,384 x 8,192, fp32 stream, post  271 us  (91 %)
+//     backward    16,384 x 4,096, fp32 stream, post  201 us  (92 %)
+//                 10,000 x 2,000, post               60 us   (62 %: issue slots)
+//                 8,000 x 16,384, fp32 stream, post  629 us  (57 %: clusters)
+//                 10,000 x 2,001, post               72 us   (51 %)
 #pragma once
 
 #include <type_traits>
