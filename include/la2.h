@@ -419,8 +419,9 @@ la2_status la2_gated_norm_backward(const void *du, const void *o, const void *ga
  * dh may be the very buffer of dh_new.  After a call without y, pass alpha =
  * 1 and dy NULL.
  *
- * Arithmetic in fp32, one rounding per output.  Errors: LA2_ERR_INVALID for
- * N < 0, D < 1, eps not above 0, unknown flags, a NULL or misaligned pointer
+ * Arithmetic in fp32, one rounding per output.  The order in which a row's
+ * sums are made is fixed for a row; where D is not a multiple of 8 it depends
+ * on the row's index modulo 8.  Errors: LA2_ERR_INVALID for N < 0, D < 1, eps not above 0, unknown flags, a NULL or misaligned pointer
  * (16 bytes), post_weight or dpost_weight without LA2_NORM_POST, a missing or
  * small workspace, an overlap other than the in-place ones;
  * LA2_ERR_UNSUPPORTED for other types or D above 16,384.  N = 0: only the

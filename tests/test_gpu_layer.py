@@ -608,6 +608,82 @@ def test_other_streams_and_graphs():
     assert la2.last_device_error() == 0
 
 
+def test_two_calls_at_once():
+    """The same calls on two streams at once, over and over: no call shares
+    anything with another."""
+    calls = [all_calls(61), all_calls(62)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[], []]
+    for _ in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(calls[i]())
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(want[i], r))
+    assert la2.last_device_error() == 0
+
+
+def test_gate_shared_by_the_batch():
+    """A gate with stride 0 over the batch, and one head's o of one token."""
+    g = gen(63)
+    o, z = randn(g, 3, 2, 5, 64, dtype=BF), randn(g, 1, 5, 128, dtype=BF)
+    du = randn(g, 3, 5, 128, dtype=BF)
+    wide = z.expand(3, 5, 128)
+    for per_head in (True, False):
+        assert torch.equal(la2.gated_norm(o, wide, per_head=per_head),
+                           la2.gated_norm(o, wide.contiguous(), per_head=per_head))
+        a = la2.gated_norm_backward(du, o, wide, per_head=per_head)
+        b = la2.gated_norm_backward(du, o, wide.contiguous(), per_head=per_head)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])   # one gradient per use
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 values: their last rows equal those of a call
+    on these rows alone."""
+    g = gen(64)
+    for D in (8192, 8191):                                # N * D just above 2^31
+        N = (1 << 31) // D + 40
+        keep = 8 + N % 8                                  # rows that begin at the same place in a 16-byte piece
+        h, y = (torch.empty(N, D, device=DEV, dtype=BF).normal_(generator=g) for _ in range(2))
+        w = torch.ones(D, device=DEV)
+        hn, n = la2.residual_norm(h, y, w, post_norm=True)
+        tail = lambda t: t[-keep:].clone()  # noqa: E731
+        a, b = la2.residual_norm(tail(h), tail(y), w, post_norm=True)
+        assert torch.equal(hn[-keep:], a) and torch.equal(n[-keep:], b)
+        dh, dy, _, _ = la2.residual_norm_backward(n, hn, y, w, dh_new=h, post_norm=True)
+        c, d, _, _ = la2.residual_norm_backward(b, a, tail(y), w, dh_new=tail(h), post_norm=True)
+        assert torch.equal(dh[-keep:], c) and torch.equal(dy[-keep:], d)
+        del h, y, hn, n, dh, dy
+        torch.cuda.empty_cache()
+    H, e, keep = 32, 64, 9
+    L = (1 << 31) // (H * e) + 50
+    o, z = torch.empty(1, H, L, e, device=DEV, dtype=BF), torch.empty(1, L, H * e, device=DEV, dtype=BF)
+    o.normal_(generator=g)
+    z.normal_(generator=g)
+    for per_head in (True, False):
+        u = la2.gated_norm(o, z, per_head=per_head)
+        end = la2.gated_norm(o[:, :, -keep:].contiguous(), z[:, -keep:].contiguous(), per_head=per_head)
+        assert torch.equal(u[:, -keep:], end)
+        do, dz, _ = la2.gated_norm_backward(u, o, z, per_head=per_head)
+        ref_do, ref_dz, _ = la2.gated_norm_backward(end, o[:, :, -keep:].contiguous(), z[:, -keep:].contiguous(), per_head=per_head)
+        assert torch.equal(do[:, :, -keep:], ref_do) and torch.equal(dz[:, -keep:], ref_dz)
+        del u, do, dz
+    f, _ = la2.rotary_frequencies(e, device=DEV)
+    q = z.unflatten(-1, (H, e)).transpose(1, 2)
+    pos = torch.arange(L, device=DEV)[None] % 1000
+    rq, rk = la2.rotary(q, q[:, :1], f, pos)
+    a, b = la2.rotary(q[:, :, -keep:], q[:, :1, -keep:], f, pos[:, -keep:].contiguous())
+    assert torch.equal(rq[:, :, -keep:], a) and torch.equal(rk[:, :, -keep:], b)
+    gq, gk = la2.rotary_backward(rq, rk, f, pos, kv_heads=4)
+    c, d = la2.rotary_backward(a, b, f, pos[:, -keep:].contiguous(), kv_heads=4)
+    assert torch.equal(gq[:, :, -keep:], c) and torch.equal(gk[:, :, -keep:], d)
+    assert la2.last_device_error() == 0
+
+
 def test_directional_derivatives():
     """The kernels' gradients along random directions against central
     differences of the fp64 losses (fp32 inputs: 1e-5 of the gradient's and
