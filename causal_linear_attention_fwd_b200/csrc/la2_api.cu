@@ -635,9 +635,13 @@ struct NormPlan {
   bool odd;
 };
 // The row's width decides who holds it (see la2_norm.cuh): a warp, a CTA of 128
-// or 256 threads with up to `most_units` units of eight values each, or a
-// cluster of CTAs.  odd: rows that begin anywhere between two 16-byte pieces
-// (up to 7 places more).
+// or 256 threads with up to `most_units` units of eight values each, 512
+// threads, or a cluster of CTAs.  odd: rows that begin anywhere between two
+// 16-byte pieces (up to 7 places more).  Measured at the borders: 128 threads
+// against 256 half of which idle, 1,000 columns backward 92 us against 102;
+// 512 threads against a cluster of two, 5,000 columns backward 150 us against
+// 219; four units (the residual norm's forward, whose rows leave the registers
+// for it) against a cluster of two, 8,192 columns 182 us against 207.
 NormPlan row_plan(int D, bool odd, int most_units = 2) {
   NormPlan g;
   g.slices = 1;
@@ -1025,7 +1029,8 @@ la2_status rotary_call(const la2_heads *q, const la2_heads *k, const la2_heads *
     while ((q.n << (q.split + 1)) <= groups && (2 << q.split) <= copies) q.split++;
   }
   // few tokens (decode): the tensors and heads of a token are spread over
-  // several CTAs
+  // several CTAs (64 tokens 6.8 us against 10.3); many: a CTA takes all of its
+  // tokens' (65,536 tokens 526 us against 552 spread)
   const int per = LANES / (d / (vec ? 16 : 2));
   const int64_t groups = (H + per - 1) / per, want = (4 * (int64_t)device_sms() + tiles - 1) / tiles;
   const dim3 grid((unsigned)tiles, (unsigned)(want < groups ? want : groups), want > 1 ? (unsigned)parts : 1u);

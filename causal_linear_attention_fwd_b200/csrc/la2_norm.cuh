@@ -364,7 +364,7 @@ struct RowSum {
           // lane j of value k's four sends it to CTAs j and j + 4
           for (int to = j; to < cl; to += 4)
             if (k < K) send(smem_u32(&s.red[turn][k][rank * NW + w]), bar, to, y);
-          bulk::wait(bar, (uses >> 1) & 1, abort);
+          mbar_wait(bar, (uses >> 1) & 1, abort);
           if (threadIdx.x == 0) mbar_expect_tx(bar, (uint32_t)(cl * NW * K * sizeof(float)));
         }
         float z[1] = {0.f};
@@ -395,7 +395,7 @@ struct RowSum {
 #pragma unroll
           for (int k = 0; k < K; k++) send(smem_u32(&s.red[turn][k][rank * NW + w]), bar, l, x[k]);
         }
-        bulk::wait(bar, (uses >> 1) & 1, abort);
+        mbar_wait(bar, (uses >> 1) & 1, abort);
         if (threadIdx.x == 0) mbar_expect_tx(bar, (uint32_t)(cl * NW * K * sizeof(float)));
 #pragma unroll
         for (int k = 0; k < K; k++) {
@@ -449,7 +449,10 @@ struct Gated {
   float eps;
 };
 
-// Rows on their way per thread, and CTAs on an SM.
+// Rows on their way per thread, and CTAs on an SM.  (65,536 x 4,096 forward:
+// two rows and four CTAs 270 us, three or four rows, so three CTAs, 287; the
+// backward per head with three rows and two CTAs 66, with three CTAs, which
+// spill, 89.)
 template <bool GRAD, Gate GATE>
 constexpr int gated_streams() { return 1 + GRAD + (GATE != GATE_NONE); }
 template <typename T, int NV>
@@ -941,7 +944,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) residual_kernel(const _
     const char *stage = ring + st * stage_bytes;
     // on a timeout the values are stale, but every thread stays in step with
     // the barriers below; the error word tells the host
-    if constexpr (RING) bulk::wait(bars + st * 8, (uint32_t)(it >> shift) & 1, abort);
+    if constexpr (RING) mbar_wait(bars + st * 8, (uint32_t)(it >> shift) & 1, abort);
 #pragma unroll
     for (int n = 0; n < NV; n++) {
       const int c = col(n);
@@ -1129,7 +1132,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) residual_kernel(const _
     if (threadIdx.x == 0 && *abort) {
       volatile int none = 0;
       for (int64_t j = it > p.stages ? it - p.stages : 0; j < it; j++)
-        bulk::wait(bars + ((uint32_t)j & shift) * 8, (uint32_t)(j >> shift) & 1, &none);
+        mbar_wait(bars + ((uint32_t)j & shift) * 8, (uint32_t)(j >> shift) & 1, &none);
     }
   }
   if constexpr (GRAD) {

@@ -24,6 +24,7 @@
 
 #include "la2_bulk.cuh"
 #include "la2_common.cuh"
+#include "la2_sm100.cuh"
 
 namespace la2 {
 namespace pool {
@@ -137,7 +138,7 @@ copy_kernel(const char *from, char *to, const int *src, const int *dst, int n, i
   bool ok = true;
   uint32_t phase = 0;
   for (int it = 0; at.layer < layers; it++) {
-    ok = bulk::wait(smem_u32(bars + at.stage), phase, abort);
+    ok = mbar_wait(smem_u32(bars + at.stage), phase, abort);
     if (!ok) break;
     const uint32_t len = length(at);
     char *base = to + (int64_t)at.layer * to_size * bytes + (int64_t)at.slab * w;
@@ -160,7 +161,7 @@ copy_kernel(const char *from, char *to, const int *src, const int *dst, int n, i
     // gave up: let this CTA's own loads land before its memory is released
     volatile int none = 0;
     for (; at.stage != ahead.stage || at.slab != ahead.slab || at.layer != ahead.layer;) {
-      bulk::wait(smem_u32(bars + at.stage), phase, &none);
+      mbar_wait(smem_u32(bars + at.stage), phase, &none);
       next(at);
       if (at.stage == 0) phase ^= 1;
     }

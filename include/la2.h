@@ -50,6 +50,9 @@
  *   - The elementwise feature-map calls (la2_feature_map,
  *     la2_feature_map_backward) take a count of values instead of shapes and
  *     may write in place; their declarations state these exceptions.
+ *   - The rotary, norm and pool-copy calls (la2_rotary, la2_gated_norm,
+ *     la2_residual_norm, their backwards, la2_pool_copy) have shapes, strided
+ *     views, in-place uses and limits of their own, stated with them.
  *
  * Errors: LA2_ERR_INVALID for bad arguments (null required pointer, negative
  * size, unaligned pointer, an output overlapping an input, kv_out == kv0,
@@ -421,8 +424,8 @@ la2_status la2_gated_norm_backward(const void *du, const void *o, const void *ga
  *
  * Arithmetic in fp32, one rounding per output.  The order in which a row's
  * sums are made is fixed for a row; where D is not a multiple of 8 it depends
- * on the row's index modulo 8.  Errors: LA2_ERR_INVALID for N < 0, D < 1, eps not above 0, unknown flags, a NULL or misaligned pointer
- * (16 bytes), post_weight or dpost_weight without LA2_NORM_POST, a missing or
+ * on the row's index modulo 8.  Errors: LA2_ERR_INVALID for N < 0, D < 1, eps
+ * not above 0, unknown flags, a NULL or misaligned pointer (16 bytes), post_weight or dpost_weight without LA2_NORM_POST, a missing or
  * small workspace, an overlap other than the in-place ones;
  * LA2_ERR_UNSUPPORTED for other types or D above 16,384.  N = 0: only the
  * weights' gradients are written (zeros).
