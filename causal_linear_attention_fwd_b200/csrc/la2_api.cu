@@ -823,7 +823,7 @@ cudaError_t residual_launch(la2::norm::Residual p, const NormPlan &g, float *dw,
   if (TPR > 32) {
     // two rows where two CTAs on an SM (one of 512 threads) have room for
     // them, else one
-    const size_t room = NT == 512 ? 227 * 1024 - 3 * 1024 : two_ctas(GRAD, ODD);
+    const size_t room = NT == 512 ? 227 * 1024 - 4 * 1024 : two_ctas(GRAD, ODD);
     p.stages = residual_smem<T, R, POST, GRAD>(p, g.cols, 2) <= room ? 2 : 1;
     smem = residual_smem<T, R, POST, GRAD>(p, g.cols, p.stages);
   } else if (GRAD) {
