@@ -18,6 +18,7 @@
 #include "la2_dlam_tc.cuh"
 #include "la2_fmap.cuh"
 #include "la2_norm.cuh"
+#include "la2_norm_plan.h"
 #include "la2_pool.cuh"
 #include "la2_rotary.cuh"
 #include "la2_shard.cuh"
@@ -588,6 +589,8 @@ la2_status fmap_call(const void *q, const void *k, const void *gq, const void *g
 // ---------------------------------------------- norms, rotary, pool copies
 namespace {
 
+using namespace la2::norm_plan;
+
 // Any byte shared by an output with an input or with another output, but for
 // an output that is exactly the input named beside it (in place).
 struct OutSpan {
@@ -627,60 +630,7 @@ int resident(K kernel, int threads, size_t smem, std::atomic<uint64_t> &last) {
 // Partial rows of weight gradients that a backward may write per SM: its
 // CTAs per SM, at most this many.
 constexpr int kNormGradPerSm = 4;
-constexpr int kNormMaxCols = 16384;  // widest row that one CTA holds
 
-// How a norm's CTAs cover rows and columns.
-struct NormPlan {
-  int nt, tpr, nv, cols, slices, cl, rpc;
-  bool odd;
-};
-// The row's width decides who holds it (see la2_norm.cuh): a warp, a CTA of 128
-// or 256 threads with up to `most_units` units of eight values each, 512
-// threads, or a cluster of CTAs.  odd: rows that begin anywhere between two
-// 16-byte pieces (up to 7 places more).  Measured at the borders: 128 threads
-// against 256 half of which idle, 1,000 columns backward 92 us against 102;
-// 512 threads against a cluster of two, 5,000 columns backward 150 us against
-// 219; four units (the residual norm's forward, whose rows leave the registers
-// for it) against a cluster of two, 8,192 columns 182 us against 207.
-NormPlan row_plan(int D, bool odd, int most_units = 2) {
-  NormPlan g;
-  g.slices = 1;
-  g.odd = odd;
-  const int places = odd ? D + 7 : D;
-  // 256 threads to a CTA, or 512 where that saves a cluster (two units each)
-  const int threads = most_units == 2 && places > 4096 ? 512 : 256, most = 8 * threads * most_units;
-  g.cl = 1;
-  while (g.cl * most < places) g.cl *= 2;
-  g.cols = ((places + 7) / 8 + g.cl - 1) / g.cl * 8;
-  if (places <= 512) {
-    g.nt = 128;
-    g.tpr = 32;
-    g.nv = 2;
-  } else if (!odd && places <= 1024) {
-    g.nt = g.tpr = 128;
-    g.nv = 1;
-  } else {
-    g.nt = g.tpr = threads;
-    g.nv = g.cols <= 2048 ? 1 : g.cols <= 16 * threads ? 2 : 4;
-  }
-  g.rpc = g.nt / g.tpr;
-  return g;
-}
-// Per head: the most heads side by side that divide H, so no lane is idle.
-NormPlan head_plan(int H, int e) {
-  NormPlan g;
-  g.odd = false;
-  g.nt = 256;
-  g.nv = 1;
-  g.cl = 1;
-  int heads = g.nt * 8 / e;
-  while (H % heads) heads /= 2;
-  g.cols = heads * e;
-  g.tpr = g.cols / 8;
-  g.slices = H / heads;
-  g.rpc = g.nt / g.tpr;
-  return g;
-}
 // Groups of CTAs (one row of partial sums each) that walk the rows.  Odd rows:
 // where a group walks more than one, they lie a multiple of 8 apart.
 int64_t norm_groups(int64_t rows, const NormPlan &g, int per_sm) {
@@ -708,7 +658,7 @@ size_t norm_ws_bytes(int op, int B, int H, int64_t L, int d, int e, la2_dtype dt
   // never more than one row of H * e
   int64_t most = norm_groups(rows, head_plan(H, e), kNormGradPerSm);
   if (D <= kNormMaxCols) {
-    const int64_t n = norm_groups(rows, row_plan((int)D, false), kNormGradPerSm);
+    const int64_t n = norm_groups(rows, gated_row_plan((int)D, (int)esize(dt)), kNormGradPerSm);
     if (n > most) most = n;
   }
   return (size_t)(most * D) * sizeof(float);
@@ -777,7 +727,7 @@ cudaError_t gated_shape(const la2::norm::Gated &p, bool row, float *dw, cudaStre
     return p.e == 64 ? gated_launch<T, 64, false, GRAD, GATE, 256, 32, 1>(p, g, dw, st)
                      : gated_launch<T, 128, false, GRAD, GATE, 256, 32, 1>(p, g, dw, st);
   }
-  const NormPlan g = row_plan(p.H * p.e, false);
+  const NormPlan g = gated_row_plan(p.H * p.e, sizeof(T));
   if (g.tpr == 32) return gated_launch<T, 0, true, GRAD, GATE, 128, 32, 2>(p, g, dw, st);
   if (g.tpr == 128) return gated_launch<T, 0, true, GRAD, GATE, 128, 128, 1>(p, g, dw, st);
   if (g.nv == 1) return gated_launch<T, 0, true, GRAD, GATE, 256, 256, 1>(p, g, dw, st);

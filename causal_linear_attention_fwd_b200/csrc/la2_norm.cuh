@@ -59,6 +59,7 @@
 #include "la2_bulk.cuh"
 #include "la2_common.cuh"
 #include "la2_fmap.cuh"
+#include "la2_norm_plan.h"
 #include "la2_sm100.cuh"
 
 namespace la2 {
@@ -476,8 +477,9 @@ __global__ void __launch_bounds__(NT, gated_ctas<T, GRAD, NT>())
 gated_kernel(const __grid_constant__ Gated p) {
   constexpr int V = 8, P = V / 2, LPH = ROW ? 32 : E / V;
   // a unit: 8 neighbours, or in fp32 twice 4 of them, 32 columns apart, so that
-  // 8 lanes move whole lines
-  constexpr int APART = sizeof(T) == 2 ? 4 : 32;
+  // 8 lanes move whole lines.  The second four have neither bounds nor a head of
+  // their own: c0 and the CTA's width are multiples of a block (gated_block).
+  constexpr int APART = norm_plan::gated_apart(sizeof(T));
   constexpr int S = gated_stages<T, NV>();
   constexpr bool HOLD = !(GRAD && NV == 2);  // the weights, in registers throughout
   using Sum = RowSum<ROW ? TPR : 32, GRAD ? 2 : 1, 4>;
@@ -514,7 +516,7 @@ gated_kernel(const __grid_constant__ Gated p) {
   };
 #pragma unroll
   for (int n = 0; n < NV; n++) {
-    c[n] = c0 + (sizeof(T) == 2 ? (n * tpr + tr) * V : (n * tpr + tr) / 8 * 64 + tr % 8 * 4);
+    c[n] = c0 + norm_plan::gated_unit(sizeof(T), n * tpr + tr);
     at_o[n] = (int64_t)(c[n] / e) * p.L * e + c[n] % e;
     if constexpr (HOLD) weights(c[n], held[n]);
     if constexpr (GRAD) {

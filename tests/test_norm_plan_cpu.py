@@ -1,0 +1,55 @@
+"""The norms' plans (csrc/la2_norm_plan.h), built as a host program: which CTA
+and thread takes which columns, over every width."""
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+GATED = r"""
+#include <cstdio>
+#include <cstring>
+#include "la2_norm_plan.h"
+using namespace la2::norm_plan;
+// The units of the CTAs that share a row (or, per head, a slice's) as the
+// kernel places them: every column once, no unit across a head's end.
+static bool covered(const NormPlan &g, int D, int e, int bytes) {
+  static char seen[1 << 16];
+  std::memset(seen, 0, sizeof seen);
+  for (int part = 0; part < g.cl * g.slices; part++) {
+    const int c0 = part * g.cols, end = c0 + g.cols < D ? c0 + g.cols : D;
+    for (int u = 0; u < g.nv * g.tpr; u++) {
+      const int c = c0 + gated_unit(bytes, u);
+      if (c >= end) continue;
+      const int last = c + gated_apart(bytes);
+      if (c / e != (last + 3) / e) return false;
+      for (int i = 0; i < 4; i++) seen[c + i]++, seen[last + i]++;
+    }
+  }
+  for (int c = 0; c < (1 << 16); c++)
+    if (seen[c] != (c < D)) return false;
+  return true;
+}
+int main() {
+  for (int e = 64; e <= 128; e += 64)
+    for (int H = 1; H * e <= kNormMaxCols; H++)
+      for (int bytes = 2; bytes <= 4; bytes += 2) {
+        if (!covered(gated_row_plan(H * e, bytes), H * e, e, bytes)) std::printf("row %d %d %d\n", H, e, bytes);
+        if (!covered(head_plan(H, e), H * e, e, bytes)) std::printf("head %d %d %d\n", H, e, bytes);
+      }
+}
+"""
+
+
+def run(tmp_path, source):
+    src, exe = tmp_path / "plan.cpp", tmp_path / "plan"
+    src.write_text(source)
+    include = os.path.join(ROOT, "causal_linear_attention_fwd_b200", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", include, "-o", str(exe), str(src)], check=True)
+    return subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
+
+
+def test_gated_rows_are_covered_once(tmp_path):
+    """Every head count and size up to the widest row, 16 and 32 bits."""
+    assert run(tmp_path, GATED) == ""
