@@ -613,6 +613,23 @@ bool all_aligned16(std::initializer_list<const void *> ps) {
 }
 bool dtype_ok(la2_dtype dt) { return dt == LA2_F32 || dt == LA2_BF16; }
 
+// Lets a kernel have all the shared memory that its static arrays leave, once
+// per device (`done`: a bit for each).  The limit belongs to the kernel, not to
+// the call: where calls of one kernel need different sizes and each set its
+// own, one thread's could fall between another's set and its launch.
+template <typename K>
+cudaError_t opt_in_all_smem(K kernel, std::atomic<uint64_t> &done) {
+  int dev = 0, most = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  cudaFuncAttributes a;
+  if (cudaError_t e = cudaFuncGetAttributes(&a, kernel)) return e;
+  if (cudaError_t e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) return e;
+  if (cudaError_t e = opt_in_smem(kernel, (size_t)most - a.sharedSizeBytes)) return e;
+  if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 // CTAs per SM of a kernel.  `last` keeps the answer for the last size of
 // shared memory asked about (size << 8 | CTAs).
 template <typename K>
@@ -703,8 +720,9 @@ template <typename T, int E, bool ROW, bool GRAD, la2::norm::Gate GATE, int NT, 
 cudaError_t gated_launch(la2::norm::Gated p, const NormPlan &g, float *dw, cudaStream_t st) {
   auto kern = la2::norm::gated_kernel<T, E, ROW, GRAD, GATE, NT, TPR, NV>;
   constexpr size_t smem = la2::norm::gated_smem<T, GRAD, GATE, NT, NV>();
+  static std::atomic<uint64_t> opted{0};
   if (smem > 32 * 1024)  // 48 KB with the static arrays go without
-    if (cudaError_t e = opt_in_smem(kern, smem)) return e;
+    if (cudaError_t e = opt_in_all_smem(kern, opted)) return e;
   static std::atomic<uint64_t> last{0};
   const int per_sm = resident(kern, NT, smem, last);
   const int64_t groups =
@@ -779,8 +797,9 @@ cudaError_t residual_launch(la2::norm::Residual p, const NormPlan &g, float *dw,
   } else if (GRAD) {
     smem = (size_t)(NT / TPR) * p.D * sizeof(float);
   }
+  static std::atomic<uint64_t> opted{0};
   if (smem > 32 * 1024)  // 48 KB with the static arrays go without
-    if (cudaError_t e = opt_in_smem(kern, smem)) return e;
+    if (cudaError_t e = opt_in_all_smem(kern, opted)) return e;
   static std::atomic<uint64_t> last{0};
   int per_sm = resident(kern, NT, smem, last);
   if (GRAD && per_sm > kNormGradPerSm) per_sm = kNormGradPerSm;
@@ -890,8 +909,9 @@ cudaError_t rotary_launch(const la2::rot::Args &a, dim3 grid, cudaStream_t st) {
   using namespace la2::rot;
   auto kern = rotary_kernel<T, GRAD, SUMS, INTER, V, U>;
   const size_t smem = (size_t)TOK * (a.r / 2) * sizeof(float2) + (SUMS ? sums_smem<T, V>() : 0);
+  static std::atomic<uint64_t> opted{0};
   if (smem > 32 * 1024)
-    if (cudaError_t e = opt_in_smem(kern, smem)) return e;
+    if (cudaError_t e = opt_in_all_smem(kern, opted)) return e;
   kern<<<grid, NT, smem, st>>>(a);
   return cudaSuccess;
 }
@@ -1851,7 +1871,8 @@ la2_status la2_pool_copy(const float *from, int from_size, float *to, int to_siz
   if (out_overlap({{{to, nt}, from}}, {{from, nf}, {src, (size_t)N * 4}, {dst, (size_t)N * 4}}))
     return LA2_ERR_INVALID;
   auto kern = la2::pool::copy_kernel;
-  if (cudaError_t er = opt_in_smem(kern, la2::pool::SMEM)) return to_status(er);
+  static std::atomic<uint64_t> opted{0};
+  if (cudaError_t er = opt_in_all_smem(kern, opted)) return to_status(er);
   return to_status(timed(K_POOL_COPY, stream, [&] {
     kern<<<(unsigned)device_sms(), la2::pool::NT, la2::pool::SMEM, stream>>>(
         reinterpret_cast<const char *>(from), reinterpret_cast<char *>(to), src, dst, N, from_size,

@@ -3,6 +3,8 @@ meet their limits: rows that two CTAs share, threads that call at once, gates
 far out, streams given by name.  Tolerances as in test_gpu_layer.py unless a
 test derives its own."""
 import math
+import struct
+import threading
 
 import pytest
 import torch
@@ -10,7 +12,7 @@ import torch
 import causal_linear_attention_fwd_b200 as la2
 import layer_ref as ref
 from layer_ref import F32, close, d64
-from test_gpu_layer import BF, DEV, FP, gated_inputs, randn
+from test_gpu_layer import BF, DEV, FP, gated_inputs, gen, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +62,45 @@ def test_gated_norm_wide_rows_of_odd_heads(case, dtype):
         close("dgate", dg, want[1], dtype, 128 * F32 * ((up.unflatten(-1, (H, e)) * ww).abs() * y * slope).flatten(2))
     if w is not None:
         close("dw", dw, want[2], FP, (B * L + 128) * F32 * ((up.unflatten(-1, (H, e)) * a).abs() * y).sum((0, 1)).flatten())
+
+
+def test_host_threads_at_different_sizes():
+    """Two host threads whose calls run the same kernels with different amounts
+    of shared memory: rows of 2,560 and 4,096 columns, 16 and 128 turned columns
+    with shared heads.  The C entries in a close loop, where one thread's set-up
+    falls into another's: every call is launched and right."""
+    g = gen(71)
+    lib, rows, B, H, L, d = la2.library(), 2, 1, 2, 3, 64
+    jobs = []
+    for D, r in ((2560, 16), (4096, 64)):
+        h, y = randn(g, rows, D), randn(g, rows, D, dtype=BF)
+        dq, dk, f = randn(g, B, H, L, d), randn(g, B, H, L, d), la2.rotary_frequencies(r, device=DEV)[0]
+        want = [*la2.residual_norm(h, y), *la2.rotary_backward(dq, dk, f, kv_heads=1)]
+        outs = [torch.zeros_like(t) for t in want]
+        p = [t.data_ptr() for t in outs]
+        side = torch.cuda.Stream()
+        head = struct.Struct("=qqqq").pack
+        gq, gk = (head(x.data_ptr(), *x.stride()[:3]) for x in outs[2:])
+        norm = (h.data_ptr(), 0, y.data_ptr(), None, None, p[0], p[1], 1.0, 1.0, 1e-6, 0, rows, D, 1, side.cuda_stream)
+        turn = (dq.data_ptr(), dk.data_ptr(), None, f.data_ptr(), None, 0, gq, gk, None, 1.0, 0, B, H, 1, L, d, d, r, 0,
+                side.cuda_stream)
+        jobs.append((norm, turn, outs, want, (h, y, dq, dk, f, side)))
+    torch.cuda.synchronize()
+    start, codes = threading.Barrier(2), [set(), set()]
+
+    def loop(i):
+        norm, turn = jobs[i][:2]
+        start.wait()
+        for call, args in ((lib.la2_residual_norm, norm), (lib.la2_rotary_backward, turn)):
+            for _ in range(20000):
+                codes[i].add(call(*args))
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{0}, {0}]
+    for _, _, outs, want, _ in jobs:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert la2.last_device_error() == 0
