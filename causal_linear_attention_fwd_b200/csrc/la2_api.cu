@@ -17,6 +17,7 @@
 #include "la2_decode.cuh"
 #include "la2_dlam_tc.cuh"
 #include "la2_fmap.cuh"
+#include "la2_memo.h"
 #include "la2_norm.cuh"
 #include "la2_norm_plan.h"
 #include "la2_pool.cuh"
@@ -630,18 +631,15 @@ cudaError_t opt_in_all_smem(K kernel, std::atomic<uint64_t> &done) {
   return cudaSuccess;
 }
 
-// CTAs per SM of a kernel.  `last` keeps the answer for the last size of
-// shared memory asked about (size << 8 | CTAs).
+// CTAs per SM of a kernel with this much dynamic shared memory, on the current
+// device.
 template <typename K>
-int resident(K kernel, int threads, size_t smem, std::atomic<uint64_t> &last) {
-  const uint64_t known = last.load(std::memory_order_relaxed);
-  if (known && known >> 8 == smem) return (int)(known & 255);
-  int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess ||
-      n < 1)
-    n = 1;
-  last.store((uint64_t)smem << 8 | (uint64_t)n, std::memory_order_relaxed);
-  return n;
+int resident(K kernel, int threads, size_t smem, la2::DeviceMemo &memo) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  return memo.get(dev, smem, 1, [&](int *n) {
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kernel, threads, smem) == cudaSuccess;
+  });
 }
 
 // Partial rows of weight gradients that a backward may write per SM: its
@@ -723,8 +721,8 @@ cudaError_t gated_launch(la2::norm::Gated p, const NormPlan &g, float *dw, cudaS
   static std::atomic<uint64_t> opted{0};
   if (smem > 32 * 1024)  // 48 KB with the static arrays go without
     if (cudaError_t e = opt_in_all_smem(kern, opted)) return e;
-  static std::atomic<uint64_t> last{0};
-  const int per_sm = resident(kern, NT, smem, last);
+  static la2::DeviceMemo memo;
+  const int per_sm = resident(kern, NT, smem, memo);
   const int64_t groups =
       norm_groups(p.rows, g, GRAD && per_sm > kNormGradPerSm ? kNormGradPerSm : per_sm);
   p.cols = g.cols;
@@ -800,8 +798,8 @@ cudaError_t residual_launch(la2::norm::Residual p, const NormPlan &g, float *dw,
   static std::atomic<uint64_t> opted{0};
   if (smem > 32 * 1024)  // 48 KB with the static arrays go without
     if (cudaError_t e = opt_in_all_smem(kern, opted)) return e;
-  static std::atomic<uint64_t> last{0};
-  int per_sm = resident(kern, NT, smem, last);
+  static la2::DeviceMemo memo;
+  int per_sm = resident(kern, NT, smem, memo);
   if (GRAD && per_sm > kNormGradPerSm) per_sm = kNormGradPerSm;
   const int64_t groups = norm_groups(p.rows, g, per_sm);
   p.cols = g.cols;

@@ -1,5 +1,6 @@
-"""The norms' plans (csrc/la2_norm_plan.h), built as a host program: which CTA
-and thread takes which columns, over every width."""
+"""The norms' plans (csrc/la2_norm_plan.h) and the answers kept about a device
+(csrc/la2_memo.h), built as host programs: which CTA and thread takes which
+columns, over every width; which questions are asked again."""
 import os
 import subprocess
 
@@ -53,3 +54,36 @@ def run(tmp_path, source):
 def test_gated_rows_are_covered_once(tmp_path):
     """Every head count and size up to the widest row, 16 and 32 bits."""
     assert run(tmp_path, GATED) == ""
+
+
+MEMO = r"""
+#include <cstdio>
+#include "la2_memo.h"
+static int asked = 0;
+static int get(la2::DeviceMemo &m, int dev, uint64_t key, bool works, int answer) {
+  return m.get(dev, key, 1, [&](int *n) { asked++; *n = answer; return works; });
+}
+int main() {
+  static la2::DeviceMemo m;
+  int bad = 0;
+  auto expect = [&](int got, int want, int questions) {
+    if (got != want || asked != questions) std::printf("%d: %d %d, %d questions\n", ++bad, got, want, asked);
+  };
+  expect(get(m, 0, 100, false, 9), 1, 1);    // failed: the stand-in, and not kept
+  expect(get(m, 0, 100, true, 4), 4, 2);
+  expect(get(m, 0, 100, true, 7), 4, 2);     // kept
+  expect(get(m, 1, 100, true, 3), 3, 3);     // another device has its own
+  expect(get(m, 0, 100, true, 7), 4, 3);
+  expect(get(m, 0, 200, true, 2), 2, 4);     // another size
+  expect(get(m, 1, 100, true, 7), 3, 4);
+  expect(get(m, 0, 0, true, 5), 5, 5);       // no shared memory is a size too
+  expect(get(m, 0, 0, true, 7), 5, 5);
+  expect(get(m, 64, 100, true, 6), 6, 6);    // past the devices that are kept, or none
+  expect(get(m, -1, 100, true, 6), 6, 7);
+  expect(get(m, 2, 100, true, 0), 1, 8);     // no CTA fits: the stand-in
+}
+"""
+
+
+def test_answers_are_kept_by_device(tmp_path):
+    assert run(tmp_path, MEMO) == ""
