@@ -104,3 +104,65 @@ def test_host_threads_at_different_sizes():
     for _, _, outs, want, _ in jobs:
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert la2.last_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("activation", ["silu", "sigmoid"])
+@pytest.mark.parametrize("per_head", [True, False])
+def test_gates_far_out(per_head, activation, dtype):
+    """Gates to +-104 and beyond.  o is +-1, so a row's norm is the one number r
+    that the call without a gate gives, and u = +-r a(g) errs by the gate's own
+    steps.  In units of 2^-24 of the value:
+      fp32   the power of two 4 (2^-22), its correction 1, 1 + e^-|g| 1, the
+             reciprocal and the product 1 each, times r 1, times g (silu) 1: 10;
+             where the result is subnormal, 4 last places (2^-149) of the
+             sigmoid, which silu multiplies by g.
+      bf16   (|g| + 4) 2 by the approximate instructions and 3 for the products,
+             half a step of the type, and below g = -87 the sigmoid's less than
+             2^-126 left out.
+    The gradient of g: the sigmoid's 8, 1 - s with s's 8 and 1 of its own, one
+    product with g and one sum, four products: under 24 of its terms; a result
+    below 2^-126 is off by half a step of the type's subnormals (2^-134, 2^-150).
+    do = r (dy - y mean(dy y)) is linear in the sigmoid, so what a sigmoid leaves
+    out enters as r (|up| lost + |y| mean(|up| lost |y|))."""
+    g = gen(72)
+    B, H, L, e = 1, 4, 40, 64
+    o = torch.where(torch.rand(B, H, L, e, generator=g, device=DEV) < 0.5, -1.0, 1.0).to(dtype)
+    z = torch.empty(B, L, H * e, device=DEV).uniform_(-104, 104, generator=g)
+    z[:, :10] = torch.linspace(-104, -80, 10 * H * e, device=DEV).view(10, H * e)
+    z[0, 10, :10] = torch.tensor([20., -20., 60., -60., 86., -86., 90., -90., 1e4, -1e4], device=DEV)
+    z = z.to(dtype)
+    du = randn(g, B, L, H * e, dtype=dtype)
+    how = dict(activation=activation, per_head=per_head)
+    r = d64(la2.gated_norm(o.float(), **how)).abs()
+    assert bool((r == r.flatten()[0]).all())
+    u = la2.gated_norm(o, z, **how)
+    do, dg, _ = la2.gated_norm_backward(du, o, z, **how)
+    assert la2.last_device_error() == 0
+    zz, y, silu = d64(z), d64(o).transpose(1, 2).flatten(2) * r, activation == "silu"
+    s = torch.sigmoid(zz)
+    a = s * zz if silu else s
+    times = 1 + zz.abs() if silu else torch.ones_like(zz)
+    if dtype == FP:
+        slack, lost = 10 * F32, 4 * 2.0 ** -149 * times
+    else:
+        slack, lost = ref.HALF[BF] + (2 * zz.abs() + 11) * F32, torch.where(zz < -87, 2.0 ** -126 * times, 0.0)
+    off = (d64(u) - y * a).abs()
+    bad = off > (1 + 2.0 ** -6) * slack * (y * a).abs() + lost
+    assert not bool(bad.any()), (int(bad.sum()), zz[bad][:4], (off / (y * a).abs())[bad][:4] / F32)
+    slope = s * (1 + zz * (1 - s)) if silu else s * (1 - s)
+    up = d64(du)
+    terms, want = (up * y).abs() * s * times, up * y * slope
+    step = 24 * F32 if dtype == FP else (2 * zz.abs() + 24) * F32
+    bound = ref.HALF[dtype] * want.abs() * (1 + 2.0 ** -6) + step * terms + (lost + 2.0 ** -149) * (1 + up.abs()) * 2
+    bound = bound + (2.0 ** -150 if dtype == FP else 2.0 ** -134)
+    off = (d64(dg) - want).abs()
+    assert bool((off <= bound).all()), (off / bound).max()
+    dy = (up * a).abs()
+    over = lambda t: t.unflatten(-1, (H, e)).mean(-1 if per_head else (-2, -1), keepdim=True).expand(B, L, H, e).flatten(2)  # noqa: E731
+    want = r * (up * a - y * over(up * a * y))
+    size = r * (dy + y.abs() * over(dy * y.abs()))
+    turn = lambda t: t.unflatten(-1, (H, e)).transpose(1, 2)  # noqa: E731
+    far = 0 if dtype == FP else 2 * 104 * F32
+    left = r * (up.abs() * lost + y.abs() * over(up.abs() * lost * y.abs()))
+    close("do", do, turn(want), dtype, turn((128 * F32 + far) * size + left))
