@@ -187,6 +187,38 @@ def _stream(stream, device=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_no_guard = contextlib.nullcontext()  # a device that is current is not made current again
+
+
+@contextlib.contextmanager
+def _named_stream(dev, stream):
+    caller = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        yield caller
+
+
+def _guard(dev, stream=None):
+    """What a call runs under: its device current and, where it names a stream
+    that is not, that stream as well: its scratch and results then come from
+    memory that this stream's earlier work is done with, and scratch goes back
+    behind the call's own work.  Gives the caller's stream then, else None."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        if stream.cuda_stream != torch._C._cuda_getCurrentRawStream(dev.index):
+            return _named_stream(dev, stream)
+    return _no_guard if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _used_on(streams, *tensors):
+    """Marks tensors (or None) as used on these streams: memory that is given
+    back before such a use has run is not handed out until it has."""
+    for t in tensors:
+        if t is not None:
+            for s in streams:
+                t.record_stream(s)
+
+
 def _out(t, name, shape, dtype, device):
     """A caller-provided output buffer: contiguous, on `device`, of this
     shape and dtype."""
@@ -609,9 +641,6 @@ LA2_NORM_SILU, LA2_NORM_ROW, LA2_NORM_SHARED_WEIGHT, LA2_NORM_POST = 1, 2, 4, 8
 # The calls below are also made for single tokens, where the host's part of a
 # call is what it costs: their checks read each property of a tensor once, and
 # a device that is already current is not made current again.
-_no_guard = contextlib.nullcontext()
-
-
 def _cuda(name, t):
     """The device of a call's first tensor."""
     if not t.is_cuda:
@@ -630,13 +659,9 @@ def _on(dev, name, t, dense=True):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _guard(dev):
-    return _no_guard if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-
 def _raw_stream(stream, dev):
     if stream is not None:
-        return _stream(stream, dev)
+        return ctypes.c_void_p(stream.cuda_stream)
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
@@ -753,7 +778,7 @@ def rotary(q, k, inv_freq, positions=None, *, v=None, interleaved: bool = False,
     if k.dtype != dtype or (v is not None and v.dtype != dtype):
         raise ValueError("q, k and v must have one dtype")
     r, kind = _rotary_args(inv_freq, positions, B, L, dev)
-    with _guard(dev):
+    with _guard(dev, stream) as caller:
         if out is None:
             rq = q.new_empty(shape)
             rk = torch.empty_like(rq)
@@ -772,6 +797,8 @@ def rotary(q, k, inv_freq, positions=None, *, v=None, interleaved: bool = False,
                               LA2_ROTARY_INTERLEAVED if interleaved else 0, B, H, Hk, L, d, e, r,
                               _dt(q), _raw_stream(stream, dev))
     _check(code, "la2_rotary")
+    if caller is not None:
+        _used_on((caller, stream), q, k, v, inv_freq, positions, rq, rk, rv)
     return (rq, rk) if v is None else (rq, rk, rv)
 
 
@@ -799,7 +826,7 @@ def rotary_backward(dq, dk, inv_freq, positions=None, *, dv=None, kv_heads=None,
     if dk.dtype != dtype or (dv is not None and dv.dtype != dtype):
         raise ValueError("dq, dk and dv must have one dtype")
     r, kind = _rotary_args(inv_freq, positions, B, L, dev)
-    with _guard(dev):
+    with _guard(dev, stream) as caller:
         shapes = ((B, H, L, d), (B, Hk, L, d), (B, Hk, L, e))[:2 if dv is None else 3]
         if out is None:
             outs = [dq.new_empty((b, n, h, w)).transpose(1, 2) for b, h, n, w in shapes]
@@ -818,6 +845,8 @@ def rotary_backward(dq, dk, inv_freq, positions=None, *, dv=None, kv_heads=None,
                                        LA2_ROTARY_INTERLEAVED if interleaved else 0, B, H, Hk, L,
                                        d, e, r, _dt(dq), _raw_stream(stream, dev))
     _check(code, "la2_rotary_backward")
+    if caller is not None:
+        _used_on((caller, stream), dq, dk, dv, inv_freq, positions, *outs)
     return tuple(outs)
 
 
@@ -854,13 +883,15 @@ def gated_norm(o, gate=None, weight=None, *, activation: str = "silu", per_head:
     lib = _lib or library()
     dev = _cuda("o", o)
     B, H, L, e, flags = _gated_args(o, gate, weight, activation, per_head, dev)
-    with _guard(dev):
+    with _guard(dev, stream) as caller:
         u = (_out(out, "out", (B, L, H * e), o.dtype, dev) if out is not None
              else o.new_empty((B, L, H * e)))
         sb, sl = (0, 0) if gate is None else _row_strides("gate", gate)
         code = lib.la2_gated_norm(o.data_ptr(), _at(gate), sb, sl, _at(weight), u.data_ptr(), eps,
                                   flags, B, H, L, e, _dt(o), _raw_stream(stream, dev))
     _check(code, "la2_gated_norm")
+    if caller is not None:
+        _used_on((caller, stream), o, gate, weight, u)
     return u
 
 
@@ -879,7 +910,7 @@ def gated_norm_backward(du, o, gate=None, weight=None, *, activation: str = "sil
     dtype = o.dtype
     if du.shape != (B, L, H * e) or du.dtype != dtype:
         raise ValueError("du must be [B,L,H*e] of o's dtype")
-    with _guard(dev):
+    with _guard(dev, stream) as caller:
         if out is not None:
             do, dgate = out
             _out(do, "do", o.shape, dtype, dev)
@@ -903,6 +934,8 @@ def gated_norm_backward(du, o, gate=None, weight=None, *, activation: str = "sil
                                            eps, flags, B, H, L, e, _dt(o), _at(workspace),
                                            _nbytes(workspace), _raw_stream(stream, dev))
     _check(code, "la2_gated_norm_backward")
+    if caller is not None:
+        _used_on((caller, stream), du, o, gate, weight, workspace, do, dgate, dw)
     return do, dgate, dw
 
 
@@ -943,7 +976,7 @@ def residual_norm(h, y=None, weight=None, *, post_norm: bool = False, post_weigh
         if y.shape != h.shape or (dtype is not None and dtype != dt):
             raise ValueError("y must match h's shape, and dtype y's")
         h_new, n = (None, None) if out is None else out
-    with _guard(dev):
+    with _guard(dev, stream) as caller:
         if h_new is not None:
             _out(h_new, "h_new", h.shape, h.dtype, dev)
         elif y is not None:
@@ -956,6 +989,8 @@ def residual_norm(h, y=None, weight=None, *, post_norm: bool = False, post_weigh
                                      _at(h_new), n.data_ptr(), alpha, beta, eps, flags, N, D,
                                      _dt(n), _raw_stream(stream, dev))
     _check(code, "la2_residual_norm")
+    if caller is not None:
+        _used_on((caller, stream), h, y, weight, post_weight, h_new, n)
     return (h if y is None else h_new), n
 
 
@@ -981,7 +1016,7 @@ def residual_norm_backward(dn, h_new, y=None, weight=None, *, dh_new=None, post_
         raise ValueError("dn and y must match h_new's shape and have one dtype")
     if dh_new is not None and (dh_new.shape != shape or dh_new.dtype != h_new.dtype):
         raise ValueError("dh_new must match h_new's shape and dtype")
-    with _guard(dev):
+    with _guard(dev, stream) as caller:
         dh, dy = (None, None) if out is None else out
         dh = (_out(dh, "dh", shape, h_new.dtype, dev) if dh is not None
               else torch.empty_like(h_new))
@@ -999,6 +1034,9 @@ def residual_norm_backward(dn, h_new, y=None, weight=None, *, dh_new=None, post_
             _at(post_weight), dh.data_ptr(), _at(dy), _at(dw), _at(dpw), alpha, beta, eps, flags,
             N, D, _dt(dn), _at(workspace), _nbytes(workspace), _raw_stream(stream, dev))
     _check(code, "la2_residual_norm_backward")
+    if caller is not None:
+        _used_on((caller, stream), dn, h_new, y, weight, dh_new, post_weight, workspace,
+                 dh, dy, dw, dpw)
     return dh, dy, dw, dpw
 
 
@@ -1026,11 +1064,13 @@ def pool_copy(pool, src, dst, *, source=None, stream=None):
     if (src.dtype != torch.int32 or src.dim() != 1 or dst.dtype != torch.int32
             or dst.shape != src.shape):
         raise ValueError("src and dst must be int32 [N]")
-    with _guard(dev):
+    with _guard(dev, stream) as caller:
         code = lib.la2_pool_copy(origin.data_ptr(), from_shape[-4], pool.data_ptr(), shape[-4],
                                  src.data_ptr(), dst.data_ptr(), src.shape[0], layers, H, d, e,
                                  _raw_stream(stream, dev))
     _check(code, "la2_pool_copy")
+    if caller is not None:
+        _used_on((caller, stream), pool, source, src, dst)
     return pool
 
 

@@ -166,3 +166,89 @@ def test_gates_far_out(per_head, activation, dtype):
     far = 0 if dtype == FP else 2 * 104 * F32
     left = r * (up.abs() * lost + y.abs() * over(up.abs() * lost * y.abs()))
     close("do", do, turn(want), dtype, turn((128 * F32 + far) * size + left))
+
+
+def busy(stream):
+    """Keeps a stream at work for some 20 ms."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(40_000_000)
+
+
+def same_size(tensors):
+    """New tensors of these sizes on the current stream, filled with 7: they take
+    the memory that has come free."""
+    return [torch.full_like(t, 7, memory_format=torch.contiguous_format) for t in tensors for _ in range(2)]
+
+
+@pytest.mark.parametrize("call", ["gated", "residual"])
+def test_scratch_of_a_call_on_a_named_stream(call):
+    """A backward named for a busy stream that is not the current one: what the
+    current stream allocates after the return meets neither its scratch nor its
+    results, and the weights' gradients are right."""
+    g = gen(73)
+    side = torch.cuda.Stream()
+    if call == "gated":
+        o, z, w, du = randn(g, 2, 4, 300, 64), randn(g, 2, 300, 256), 1 + randn(g, 256, scale=.2), randn(g, 2, 300, 256)
+        run = lambda **kw: la2.gated_norm_backward(du, o, z, w, **kw)  # noqa: E731
+        n = la2.workspace_size(la2.LA2_OP_GATED_NORM_BACKWARD, 2, 4, 300, 64, 64, FP)
+    else:
+        h, y, dn, w = randn(g, 500, 1024), randn(g, 500, 1024), randn(g, 500, 1024), 1 + randn(g, 1024, scale=.2)
+        run = lambda **kw: la2.residual_norm_backward(dn, h, y, w, dh_new=y, post_norm=True, post_weight=w, **kw)  # noqa: E731
+        n = la2.workspace_size(la2.LA2_OP_RESIDUAL_NORM_BACKWARD, 1, 1, 500, 1024, 1024, FP)
+    want = run()
+    torch.cuda.synchronize()
+    busy(side)
+    got = run(stream=side)
+    others = same_size([torch.empty(n // 4, device=DEV) for _ in range(4)] + list(got))
+    torch.cuda.synchronize()
+    assert all(bool((t == 7).all()) for t in others)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_memory_of_a_call_on_a_named_stream():
+    """Inputs dropped while a named stream has yet to read them, and results
+    dropped while the caller's has: neither's memory is handed out before."""
+    g = gen(74)
+    side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+    B, H, L, d = 2, 4, 200, 64
+    f, _ = la2.rotary_frequencies(d, device=DEV)
+    src, dst = torch.tensor([1, 0], dtype=torch.int32, device=DEV), torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    x = [randn(g, B, H, L, d) for _ in range(3)]
+    z, w, pool = randn(g, B, L, H * d), 1 + randn(g, H * d, scale=.2), randn(g, 3, H, d, d)
+
+    def all_of(stream=None):
+        q, k, v = (t.clone() for t in x)
+        zz, ww, h = z.clone(), w.clone(), z + 1
+        main.synchronize()
+        if stream is not None:
+            busy(stream)
+        kw = dict(stream=stream)
+        r = list(la2.rotary(q, k, f.clone(), v=v, **kw))
+        r += la2.rotary_backward(q, k, f.clone(), dv=v, **kw)
+        r.append(la2.gated_norm(v, zz, ww, **kw))
+        r += la2.gated_norm_backward(zz, v, zz, ww, **kw)
+        r += la2.residual_norm(h, zz, ww, **kw)
+        r += la2.residual_norm_backward(zz, h, None, ww, **kw)[:3]
+        copy = pool.clone()
+        main.synchronize()
+        r.append(la2.pool_copy(copy, src.clone(), dst.clone(), **kw))
+        return r
+    want = all_of()
+    torch.cuda.synchronize()
+    got = all_of(side)                                    # its inputs are dropped by now
+    taken = same_size(x + [z, w, pool, f.float(), src])
+    main.wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda.synchronize()
+    del taken, got
+    got = all_of(side)
+    main.wait_stream(side)
+    busy(main)
+    kept = [t.clone() for t in got]                       # read when main gets there
+    shapes = [torch.empty(t.shape, device="meta") for t in got]
+    del got
+    with torch.cuda.stream(side):
+        over = [torch.full(s.shape, 7.0, device=DEV) for s in shapes for _ in range(2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(kept, want))
+    assert len(over) == 2 * len(want) and la2.last_device_error() == 0
