@@ -4,6 +4,10 @@ Argument marshalling only: every step of the computation runs in the CUDA
 kernels of libla2.so.  PyTorch supplies device memory (outputs, scratch
 workspace) and the current CUDA stream.  There is no fallback: if the
 library is missing or a call fails, an exception is raised.
+
+A call launches on the current stream, or on the one given as `stream`.  The
+caller orders a stream that it names behind what made the inputs, and what uses
+the results behind it; inputs, results and scratch may be dropped at any time.
 """
 from __future__ import annotations
 
@@ -261,7 +265,7 @@ def forward(q, k, v, lam, kv0=None, *, want_state: bool = False, out=None,
         raise ValueError("lam must be float32 [H]")
     if kv0 is not None and (kv0.dtype != torch.float32 or kv0.shape != (B, H, d, e)):
         raise ValueError("kv0 must be float32 [B,H,d,e]")
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         o = (_out(out, "out", (B, H, L, e), q.dtype, dev) if out is not None
              else torch.empty((B, H, L, e), dtype=q.dtype, device=dev))
         st = torch.empty((B, H, d, e), dtype=torch.float32, device=dev) if want_state else None
@@ -273,6 +277,8 @@ def forward(q, k, v, lam, kv0=None, *, want_state: bool = False, out=None,
                                0 if ws is None else ws.numel() * ws.element_size(),
                                _stream(stream, dev))
     _check(code, "la2_forward")
+    if caller is not None:
+        _used_on((caller, stream), q, k, v, lam, kv0, ws, o, st)
     return (o, st) if want_state else o
 
 
@@ -295,7 +301,7 @@ def forward_noalloc(q, k, v, lam, kv0=None, *, want_state: bool = False, out=Non
         raise ValueError("kv0 must be float32 [B,H,d,e]")
     if state_out is not None and not want_state:
         raise ValueError("state_out is given but want_state is False")
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         o = (_out(out, "out", (B, H, L, e), q.dtype, dev) if out is not None
              else torch.empty((B, H, L, e), dtype=q.dtype, device=dev))
         st = None
@@ -306,6 +312,8 @@ def forward_noalloc(q, k, v, lam, kv0=None, *, want_state: bool = False, out=Non
         code = lib.la2_forward_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(kv0), _ptr(o),
                                        _ptr(st), B, H, L, d, e, _dt(q), _stream(stream, dev))
     _check(code, "la2_forward_noalloc")
+    if caller is not None:
+        _used_on((caller, stream), q, k, v, lam, kv0, o, st)
     return (o, st) if want_state else o
 
 
@@ -329,7 +337,7 @@ def backward(q, k, v, lam, dO, kv0=None, *, want_dkv0: bool = False, outs=None,
         raise ValueError("lam must be float32 [H]")
     if kv0 is not None and (kv0.dtype != torch.float32 or kv0.shape != (B, H, d, e)):
         raise ValueError("kv0 must be float32 [B,H,d,e]")
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         if outs is not None:
             dq, dk, dv = outs
             _out(dq, "dq", q.shape, q.dtype, dev)
@@ -347,6 +355,8 @@ def backward(q, k, v, lam, dO, kv0=None, *, want_dkv0: bool = False, outs=None,
                                    0 if ws is None else ws.numel() * ws.element_size(),
                                    1 if reuse_forward_states else 0, _stream(stream, dev))
     _check(code, "la2_backward")
+    if caller is not None:
+        _used_on((caller, stream), q, k, v, lam, dO, kv0, ws, dq, dk, dv, dkv0)
     return (dq, dk, dv, dkv0) if want_dkv0 else (dq, dk, dv)
 
 
@@ -374,7 +384,7 @@ def forward_varlen(q, k, v, lam, cu_seqlens, kv0=None, *, want_state: bool = Fal
     [N,H,d,e].  Returns o [H,T,e] (and the final states)."""
     lib = library()
     dev, N, H, T, d, e = _varlen_args(q, k, v, lam, cu_seqlens, kv0)
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         o = (_out(out, "out", (H, T, e), q.dtype, dev) if out is not None
              else torch.empty((H, T, e), dtype=q.dtype, device=dev))
         st = torch.empty((N, H, d, e), dtype=torch.float32, device=dev) if want_state else None
@@ -382,6 +392,8 @@ def forward_varlen(q, k, v, lam, cu_seqlens, kv0=None, *, want_state: bool = Fal
                                       _ptr(kv0), _ptr(o), _ptr(st), N, H, T, d, e, _dt(q),
                                       _stream(stream, dev))
     _check(code, "la2_forward_varlen")
+    if caller is not None:
+        _used_on((caller, stream), q, k, v, lam, cu_seqlens, kv0, o, st)
     return (o, st) if want_state else o
 
 
@@ -392,7 +404,7 @@ def backward_varlen(q, k, v, lam, cu_seqlens, dO, kv0=None, *, want_dkv0: bool =
     dev, N, H, T, d, e = _varlen_args(q, k, v, lam, cu_seqlens, kv0, ("dO", dO))
     if dO.shape != v.shape:
         raise ValueError("dO must match v")
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         if outs is not None:
             dq, dk, dv = outs
             _out(dq, "dq", q.shape, q.dtype, dev)
@@ -405,6 +417,8 @@ def backward_varlen(q, k, v, lam, cu_seqlens, dO, kv0=None, *, want_dkv0: bool =
                                        _ptr(kv0), _ptr(dO), _ptr(dq), _ptr(dk), _ptr(dv),
                                        _ptr(dkv0), N, H, T, d, e, _dt(q), _stream(stream, dev))
     _check(code, "la2_backward_varlen")
+    if caller is not None:
+        _used_on((caller, stream), q, k, v, lam, cu_seqlens, dO, kv0, dq, dk, dv, dkv0)
     return (dq, dk, dv, dkv0) if want_dkv0 else (dq, dk, dv)
 
 
@@ -436,7 +450,7 @@ def forward_pool(q, k, v, lam, pool, slots, *, continue_state: bool = False, out
     if pool.dtype != torch.float32 or pool.dim() != 4 or pool.shape[1:] != (H, d, e):
         raise ValueError("pool must be float32 [P,H,d,e]")
     slots = _slots(slots, B)
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         o = (_out(out, "out", (B, H, L, e), q.dtype, dev) if out is not None
              else torch.empty((B, H, L, e), dtype=q.dtype, device=dev))
         ws = workspace
@@ -449,6 +463,8 @@ def forward_pool(q, k, v, lam, pool, slots, *, continue_state: bool = False, out
                                     0 if ws is None else ws.numel() * ws.element_size(),
                                     _stream(stream, dev))
     _check(code, "la2_forward_pool")
+    if caller is not None:
+        _used_on((caller, stream), q, k, v, lam, pool, slots, ws, o)
     return o
 
 
@@ -466,13 +482,15 @@ def decode_tokens(q, k, v, lam, pool, slots=None, *, out=None, stream=None):
     if pool.dtype != torch.float32 or pool.dim() != 4 or pool.shape[1:] != (H, d, e):
         raise ValueError("pool must be float32 [P,H,d,e]")
     slots = _slots(slots, B)
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         o = (_out(out, "out", (B, H, T, e), q.dtype, dev) if out is not None
              else torch.empty((B, H, T, e), dtype=q.dtype, device=dev))
         code = lib.la2_decode_tokens(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(pool),
                                      _ptr(slots), pool.shape[0], _ptr(o), B, H, T, d, e, _dt(q),
                                      _stream(stream, dev))
     _check(code, "la2_decode_tokens")
+    if caller is not None:
+        _used_on((caller, stream), q, k, v, lam, pool, slots, o)
     return o
 
 
@@ -486,7 +504,7 @@ def shard_state(a, b, lam, *, reverse: bool = False, workspace=None, stream=None
     e = b.shape[-1]
     if b.shape[:3] != (B, H, L):
         raise ValueError("shape mismatch between a and b")
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         out = torch.empty((B, H, d, e), dtype=torch.float32, device=dev)
         ws = workspace
         if ws is None:
@@ -496,6 +514,8 @@ def shard_state(a, b, lam, *, reverse: bool = False, workspace=None, stream=None
                                    0 if ws is None else ws.numel() * ws.element_size(),
                                    _stream(stream, dev))
     _check(code, "la2_shard_state")
+    if caller is not None:
+        _used_on((caller, stream), a, b, lam, ws, out)
     return out
 
 
@@ -510,12 +530,14 @@ def state_prefix(delta, lam, L_shard: int, kv0=None, *, reverse: bool = False, s
     R, B, H, d, e = delta.shape
     if kv0 is not None and (kv0.dtype != torch.float32 or kv0.shape != (B, H, d, e)):
         raise ValueError("kv0 must be float32 [B,H,d,e]")
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         out = torch.empty_like(delta)
         code = lib.la2_state_prefix(_ptr(delta), _ptr(kv0), _ptr(lam), _ptr(out), R, B, H,
                                     int(L_shard), d, e, 1 if reverse else 0,
                                     _stream(stream, dev))
     _check(code, "la2_state_prefix")
+    if caller is not None:
+        _used_on((caller, stream), delta, lam, kv0, out)
     return out
 
 
@@ -533,7 +555,7 @@ def backward_shard(q, k, v, lam, dO, kv0=None, dstate_end=None, *, want_dkv0: bo
     for name, t in (("kv0", kv0), ("dstate_end", dstate_end)):
         if t is not None and (t.dtype != torch.float32 or t.shape != (B, H, d, e)):
             raise ValueError(f"{name} must be float32 [B,H,d,e]")
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         if outs is not None:
             dq, dk, dv = outs
             _out(dq, "dq", q.shape, q.dtype, dev)
@@ -551,6 +573,8 @@ def backward_shard(q, k, v, lam, dO, kv0=None, dstate_end=None, *, want_dkv0: bo
                                       0 if ws is None else ws.numel() * ws.element_size(), 0,
                                       _stream(stream, dev))
     _check(code, "la2_backward_shard")
+    if caller is not None:
+        _used_on((caller, stream), q, k, v, lam, dO, kv0, dstate_end, ws, dq, dk, dv, dkv0)
     return (dq, dk, dv, dkv0) if want_dkv0 else (dq, dk, dv)
 
 
@@ -570,21 +594,22 @@ def dlambda(q, k, v, lam, dO, kv0=None, *, workspace=None, chunked: bool = True,
         raise ValueError("lam must be float32 [H]")
     if kv0 is not None and (kv0.dtype != torch.float32 or kv0.shape != (B, H, d, e)):
         raise ValueError("kv0 must be float32 [B,H,d,e]")
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         out = torch.empty(H, dtype=torch.float32, device=dev)
         if not chunked:
             code = lib.la2_backward_dlambda(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(kv0),
                                             _ptr(dO), _ptr(out), B, H, L, d, e, _dt(q),
                                             _stream(stream, dev))
-            _check(code, "la2_backward_dlambda")
-            return out
-        if workspace is None:
-            workspace = _workspace(workspace_size(LA2_OP_DLAMBDA, B, H, L, d, e, q.dtype), dev)
-        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        code = lib.la2_backward_dlambda_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(kv0),
-                                           _ptr(dO), _ptr(out), B, H, L, d, e, _dt(q),
-                                           _ptr(workspace), nbytes, _stream(stream, dev))
-    _check(code, "la2_backward_dlambda_ex")
+        else:
+            if workspace is None:
+                workspace = _workspace(workspace_size(LA2_OP_DLAMBDA, B, H, L, d, e, q.dtype), dev)
+            code = lib.la2_backward_dlambda_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(kv0),
+                                               _ptr(dO), _ptr(out), B, H, L, d, e, _dt(q),
+                                               _ptr(workspace), _nbytes(workspace),
+                                               _stream(stream, dev))
+    _check(code, "la2_backward_dlambda_ex" if chunked else "la2_backward_dlambda")
+    if caller is not None:
+        _used_on((caller, stream), q, k, v, lam, dO, kv0, workspace, out)
     return out
 
 
@@ -603,13 +628,15 @@ def feature_map(q, k=None, *, out=None, stream=None):
     out: (phi_q, phi_k) buffers, which may be q and k themselves (in place)."""
     lib = library()
     dev = _fmap_args(q, k, ())
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         phi_q, phi_k = out if out is not None else (
             torch.empty_like(q), None if k is None else torch.empty_like(k))
         _fmap_args(q, k, (("phi_q", phi_q), ("phi_k", phi_k)))
         code = lib.la2_feature_map(_ptr(q), _ptr(k), _ptr(phi_q), _ptr(phi_k), q.numel(),
                                    _dt(q), _stream(stream, dev))
     _check(code, "la2_feature_map")
+    if caller is not None:
+        _used_on((caller, stream), q, k, phi_q, phi_k)
     return phi_q if k is None else (phi_q, phi_k)
 
 
@@ -622,7 +649,7 @@ def feature_map_backward(q, k, dphi_q, dphi_k=None, *, out=None, stream=None):
     if (k is None) != (dphi_k is None):
         raise ValueError("k and dphi_k are both given or both None")
     dev = _fmap_args(q, k, (("dphi_q", dphi_q), ("dphi_k", dphi_k)))
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         dq, dk = out if out is not None else (
             torch.empty_like(q), None if k is None else torch.empty_like(k))
         _fmap_args(q, k, (("dphi_q", dphi_q), ("dphi_k", dphi_k), ("dq", dq), ("dk", dk)))
@@ -630,6 +657,8 @@ def feature_map_backward(q, k, dphi_q, dphi_k=None, *, out=None, stream=None):
                                             _ptr(dq), _ptr(dk), q.numel(), _dt(q),
                                             _stream(stream, dev))
     _check(code, "la2_feature_map_backward")
+    if caller is not None:
+        _used_on((caller, stream), q, k, dphi_q, dphi_k, dq, dk)
     return dq if k is None else (dq, dk)
 
 
@@ -1082,12 +1111,14 @@ def decode_step(q, k, v, lam, kv, *, out=None, stream=None):
     e = v.shape[-1]
     if kv.dtype != torch.float32 or kv.shape != (B, H, d, e):
         raise ValueError("kv must be float32 [B,H,d,e]")
-    with torch.cuda.device(dev):
+    with _guard(dev, stream) as caller:
         o = (_out(out, "out", (B, H, e), q.dtype, dev) if out is not None
              else torch.empty((B, H, e), dtype=q.dtype, device=dev))
         code = lib.la2_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(lam), _ptr(kv), _ptr(o),
                                    B, H, d, e, _dt(q), _stream(stream, dev))
     _check(code, "la2_decode_step")
+    if caller is not None:
+        _used_on((caller, stream), q, k, v, lam, kv, o)
     return o
 
 
