@@ -593,7 +593,9 @@ namespace {
 using namespace la2::norm_plan;
 
 // Any byte shared by an output with an input or with another output, but for
-// an output that is exactly the input named beside it (in place).
+// an output that is exactly the input named beside it (in place).  Another input
+// at that place has to be of the same length: rows of another type would lie
+// elsewhere, and one row's output on rows not yet read.
 struct OutSpan {
   Span s;
   const void *over;  // the one input whose very buffer it may be, or null
@@ -601,7 +603,8 @@ struct OutSpan {
 bool out_overlap(std::initializer_list<OutSpan> outs, std::initializer_list<Span> ins) {
   for (const OutSpan *o = outs.begin(); o != outs.end(); o++) {
     for (const Span &i : ins)
-      if (overlaps(o->s, i) && !(o->over && o->over == i.p && o->s.p == i.p)) return true;
+      if (overlaps(o->s, i) && !(o->over && o->over == i.p && o->s.p == i.p && o->s.n == i.n))
+        return true;
     for (const OutSpan *q = o + 1; q != outs.end(); q++)
       if (overlaps(o->s, q->s)) return true;
   }

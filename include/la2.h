@@ -411,7 +411,8 @@ la2_status la2_gated_norm_backward(const void *du, const void *o, const void *ga
  * h_new of type h_dt, y and n of type dt (h_dt = dt, or LA2_F32 with dt =
  * LA2_BF16); weights fp32 [D] or NULL (ones).  n comes from the sum before it
  * is rounded to h_dt.  y and h_new both NULL: n is the norm of h (alpha, beta
- * unused).  In place: h_new may be the very buffer of h, n that of y.
+ * unused).  In place: h_new may be the very buffer of h, n that of y; where h_dt
+ * = dt, h and y may be one buffer.
  *
  * la2_residual_norm_backward: from dn (of n's shape and type) and dh_new (of
  * h_new's; NULL: zero), with h_new as stored, the gradients dh (h_dt) and,
@@ -425,8 +426,9 @@ la2_status la2_gated_norm_backward(const void *du, const void *o, const void *ga
  * Arithmetic in fp32, one rounding per output.  The order in which a row's
  * sums are made is fixed for a row; where D is not a multiple of 8 it depends
  * on the row's index modulo 8.  Errors: LA2_ERR_INVALID for N < 0, D < 1, eps
- * not above 0, unknown flags, a NULL or misaligned pointer (16 bytes), post_weight or dpost_weight without LA2_NORM_POST, a missing or
- * small workspace, an overlap other than the in-place ones;
+ * not above 0, unknown flags, a NULL or misaligned pointer (16 bytes),
+ * post_weight or dpost_weight without LA2_NORM_POST, a missing or small
+ * workspace, an overlap other than the in-place ones;
  * LA2_ERR_UNSUPPORTED for other types or D above 16,384.  N = 0: only the
  * weights' gradients are written (zeros).
  */

@@ -252,3 +252,24 @@ def test_memory_of_a_call_on_a_named_stream():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(kept, want))
     assert len(over) == 2 * len(want) and la2.last_device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 99, 2048, 5001, 16384])
+def test_one_tensor_as_stream_and_block_output(D):
+    """h and y one tensor, and an output over both; the gradients of n and h' one
+    tensor, and dh over both: the bits of the call on copies."""
+    g = gen(75)
+    x, w = randn(g, 300, D), 1 + randn(g, D, scale=.2)
+    how = dict(post_norm=True, post_weight=w, alpha=0.5, beta=2.0)
+    hn, n = la2.residual_norm(x, x.clone(), w, **how)
+    for which in (0, 1):
+        y = x.clone()
+        outs = (y, torch.empty_like(y)) if which == 0 else (torch.empty_like(y), y)
+        la2.residual_norm(y, y, w, out=outs, **how)
+        assert torch.equal(outs[0], hn) and torch.equal(outs[1], n)
+    up = randn(g, 300, D)
+    want = la2.residual_norm_backward(up, hn, x, w, dh_new=up.clone(), **how)
+    over = up.clone()
+    got = la2.residual_norm_backward(over, hn, x, w, dh_new=over, out=(over, None), **how)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert la2.last_device_error() == 0
