@@ -29,10 +29,11 @@
 // own next values into shared memory, the residual norm (contiguous rows)
 // takes them by bulk copies into a ring of rows there.
 //
-// A row is held by a warp (up to 512 columns), a CTA (up to 4,096, or 8,192 in
-// the residual norm's forward) or a cluster of 2 to 8 CTAs that add their
-// partial sums through distributed shared memory: a thread's share, and so
-// the registers it takes, stays bounded at every width.
+// A row is held by a warp (up to 512 columns), a CTA (up to 8,192: 512 threads
+// of two units from 4,097 on, or in the residual norm's forward 256 of four) or
+// a cluster of 2 CTAs (4 for rows of more than 16,377 columns that 8 does not
+// divide) that add their partial sums through distributed shared memory: a
+// thread's share, and so the registers it takes, stays bounded at every width.
 //
 // The weights' gradients are column sums over all rows.  A thread keeps its
 // columns over all rows its CTA walks, so each CTA (or cluster) writes one row
@@ -337,7 +338,7 @@ struct RowSum {
   static constexpr int NW = TPR / 32;
   struct Shared {
     uint64_t bars[2];
-    float red[2][K][TPR > 32 ? (MAXCL * NW > 64 ? 64 : MAXCL * NW) : 1];
+    float red[2][K][TPR > 32 ? MAXCL * NW : 1];
   };
   uint32_t uses = 0;
   // before the first sum, by all threads; a barrier of the CTA (cl = 1: none
@@ -509,7 +510,7 @@ gated_kernel(const __grid_constant__ Gated p) {
   constexpr int APART = norm_plan::gated_apart(sizeof(T));
   constexpr int S = gated_stages<T, NV>();
   constexpr bool HOLD = !(GRAD && NV == 2);  // the weights, in registers throughout
-  using Sum = RowSum<ROW ? TPR : 32, GRAD ? 2 : 1, 4>;
+  using Sum = RowSum<ROW ? TPR : 32, GRAD ? 2 : 1, norm_plan::most_cl(false)>;
   __shared__ typename Sum::Shared red;
   extern __shared__ __align__(128) char dyn[];
   Sum row_sum;
@@ -816,8 +817,8 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) residual_kernel(const _
   constexpr bool RING = TPR > 32;
   constexpr bool HAS_Y = !GRAD || POST;  // y may be read
   constexpr int RPC = NT / TPR, P = 4;
-  // 16,384 columns take four CTAs, the up to 7 places more of odd rows eight
-  using Sum = RowSum<TPR, !GRAD ? 1 : POST ? 6 : 2, ODD ? 8 : 4, GRAD && POST && (NV == 1 || NT == 512)>;
+  using Sum = RowSum<TPR, !GRAD ? 1 : POST ? 6 : 2, norm_plan::most_cl(ODD),
+                     GRAD && POST && (NV == 1 || NT == 512)>;
   __shared__ typename Sum::Shared red;
   extern __shared__ __align__(128) char dyn[];
   Sum sum;

@@ -33,8 +33,8 @@ constexpr int gated_unit(int value_bytes, int u) {
 // for it) against a cluster of two, 8,192 columns 182 us against 207.
 // block: columns that a unit's eight values come from; no CTA of a cluster
 // begins inside one.
-inline NormPlan row_plan(int D, bool odd, int most_units = 2, int block = 8) {
-  NormPlan g;
+constexpr NormPlan row_plan(int D, bool odd, int most_units = 2, int block = 8) {
+  NormPlan g{};
   g.slices = 1;
   g.odd = odd;
   const int places = odd ? D + 7 : D;
@@ -56,6 +56,14 @@ inline NormPlan row_plan(int D, bool odd, int most_units = 2, int block = 8) {
   }
   g.rpc = g.nt / g.tpr;
   return g;
+}
+// The most CTAs that share a row: the widest one's (up to 4,096 columns, or
+// 8,192 with 512 threads or four units, stay with one).
+constexpr int most_cl(bool odd) {
+  return odd ? row_plan(kNormMaxCols - 1, true).cl
+             : row_plan(kNormMaxCols, false, 2).cl > row_plan(kNormMaxCols, false, 4).cl
+                   ? row_plan(kNormMaxCols, false, 2).cl
+                   : row_plan(kNormMaxCols, false, 4).cl;
 }
 // The gated norm's rows of H * e columns: every CTA begins at a block and holds
 // whole ones, so no unit leaves its head or meets another CTA's columns.

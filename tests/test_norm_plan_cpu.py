@@ -87,3 +87,32 @@ int main() {
 
 def test_answers_are_kept_by_device(tmp_path):
     assert run(tmp_path, MEMO) == ""
+
+
+RESIDUAL = r"""
+#include <cstdio>
+#include "la2_norm_plan.h"
+using namespace la2::norm_plan;
+static_assert(most_cl(false) >= 1 && most_cl(true) >= 1, "known to the compiler");
+int main() {
+  for (int D = 1; D <= kNormMaxCols; D++)
+    for (int odd = 0; odd <= (D % 8 != 0); odd++) {
+      if (D % 8 != 0 && !odd) continue;
+      for (int units = 2; units <= (odd ? 2 : 4); units += 2) {
+        const NormPlan g = row_plan(D, odd, units);
+        const int places = odd ? D + 7 : D;
+        // every place has a thread, every CTA a column, and the arrays of
+        // partial sums room for the cluster
+        const bool ok = g.cols % 8 == 0 && g.cl * g.cols >= places && (g.cl - 1) * g.cols < D &&
+                        g.tpr * g.nv * 8 >= g.cols && g.nt == g.tpr * g.rpc && g.cl <= most_cl(odd) &&
+                        (g.cl == 1 || g.rpc == 1);
+        if (!ok) std::printf("%d %d %d\n", D, odd, units);
+      }
+    }
+}
+"""
+
+
+def test_rows_have_threads_and_room(tmp_path):
+    """Every width, the forward's four units and the backward's two."""
+    assert run(tmp_path, RESIDUAL) == ""
