@@ -3,7 +3,10 @@ meet their limits: rows that two CTAs share, threads that call at once, gates
 far out, streams given by name.  Tolerances as in test_gpu_layer.py unless a
 test derives its own."""
 import math
+import os
 import struct
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -273,3 +276,46 @@ def test_one_tensor_as_stream_and_block_output(D):
     got = la2.residual_norm_backward(over, hn, x, w, dh_new=over, out=(over, None), **how)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert la2.last_device_error() == 0
+
+
+@pytest.mark.parametrize("D", [96, 99, 2048, 2049, 16384])
+def test_one_weight_of_two(D):
+    """A norm on y with one of the two weights: the other's gradient is not made,
+    and this one's has the bits of the call with ones for the other."""
+    g = gen(76)
+    hn, y, dn, up = (randn(g, 700, D) for _ in range(4))
+    w, one = 1 + randn(g, D, scale=.2), torch.ones(D, device=DEV)
+    how = dict(dh_new=up, post_norm=True)
+    full = la2.residual_norm_backward(dn, hn, y, w, post_weight=one, **how)
+    got = la2.residual_norm_backward(dn, hn, y, w, **how)
+    assert got[3] is None and all(torch.equal(a, b) for a, b in zip(got[:3], full))
+    full = la2.residual_norm_backward(dn, hn, y, one, post_weight=w, **how)
+    got = la2.residual_norm_backward(dn, hn, y, None, post_weight=w, **how)
+    assert got[2] is None and all(torch.equal(got[i], full[i]) for i in (0, 1, 3))
+    assert la2.last_device_error() == 0
+
+
+FIRST = """
+import torch
+import causal_linear_attention_fwd_b200 as la2
+import test_gpu_layer as t
+call = t.all_calls(81)
+h, y = t.randn(t.gen(82), 5, 4096), t.randn(t.gen(82), 5, 4096)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = call() + list(la2.residual_norm(h, y, post_norm=True)) + list(la2.residual_norm_backward(h, y, None)[:2])
+graph.replay()
+torch.cuda.synchronize()
+want = call() + list(la2.residual_norm(h, y, post_norm=True)) + list(la2.residual_norm_backward(h, y, None)[:2])
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and la2.last_device_error() == 0
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_captured():
+    """No call before the capture: what a first call sets up is allowed there."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": os.pathsep.join((here, os.path.dirname(here)))})
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
