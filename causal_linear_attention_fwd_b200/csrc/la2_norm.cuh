@@ -50,9 +50,13 @@
 //   residual norm 65,536 x 4,096                     351 us  (94 %)
 //                 16,384 x 8,192, fp32 stream, post  271 us  (91 %)
 //     backward    16,384 x 4,096, fp32 stream, post  201 us  (92 %)
-//                 10,000 x 2,000, post               60 us   (62 %: issue slots)
-//                 8,000 x 16,384, fp32 stream, post  629 us  (57 %: clusters)
-//                 10,000 x 2,001, post               72 us   (51 %)
+//                 10,000 x 2,000, post               59 us   (62 %: 56
+//                 instructions a value, issue slots 62 % busy)
+//                 8,000 x 16,384, fp32 stream, post  631 us  (57 %: one ring stage
+//                 and one CTA an SM)
+//                 10,000 x 2,001, post               71 us   (52 %)
+//                 65,536 x 256, 65,536 x 64, post    61, 52 us (51, 15 %: lanes
+//                 or their second units idle, no row ahead in a warp)
 #pragma once
 
 #include <type_traits>

@@ -18,8 +18,9 @@
 // is refilled by the very thread whose stores read it.
 //
 // Measured on B200 (states of 4 MiB, cold L2, of the copy bandwidth): a cycle
-// through 200 slots 272 us (94 %), 256 beams 265 us (88 %); a cycle through
-// 1,000 states of 256 KiB 181 us (44 %: slabs of 64 bytes).
+// through 200 slots 270 us (95 %), 256 beams 268 us (87 %); cycles through 512 and
+// 1,000 states of 256 KiB 78 and 180 us (53 and 45 %: pieces of 128 and 96
+// bytes).
 #pragma once
 
 #include "la2_bulk.cuh"

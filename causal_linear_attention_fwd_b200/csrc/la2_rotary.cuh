@@ -19,10 +19,13 @@
 // shared memory, and all heads of the token read it.
 //
 // Measured on B200 (cold L2, of the copy bandwidth): q, k, v of 65,536 tokens x
-// 32 heads x 128 in bf16 524 us (94 %); 8,192 tokens 76 us (81 %, of which the
-// launch is some 6); one token of 64 requests x 16 heads 6.8 us; the backward
-// of 16,388 tokens with 32 q heads on 8 k, v heads 113 us (70 %: bound by the
-// latency of a CTA's loads, 16 warps an SM at 127 registers).
+// 32 heads x 128 in bf16 522 us (94 %), 32,768 in fp32 535 us (92 %); 8,192
+// tokens 76 us (81 %, of which the launch is some 6); one token of 64 requests x
+// 16 heads 6.1 us; 16,384 tokens with 20 or 62 columns turned, one by one, 268 us
+// (46 %).  The backward of 16,388 tokens with 32 heads each 140 us (88 %), fp32
+// 270 us (91 %); with 32 q heads on 8 k, v heads of 64 columns 115 us (69 %: bound
+// by the latency of a CTA's loads, 16 warps an SM at 127 registers), on one of
+// 128 127 us (66 %).
 #pragma once
 
 #include "la2_common.cuh"
