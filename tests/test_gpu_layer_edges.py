@@ -319,3 +319,38 @@ def test_first_calls_of_a_process_captured():
     r = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, timeout=300,
                        env={**os.environ, "PYTHONPATH": os.pathsep.join((here, os.path.dirname(here)))})
     assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_named_stream_inside_a_capture():
+    """A capture that forks to a named stream and joins it again: scratch and
+    results come from the graph's memory, and every replay gives the bits of the
+    eager calls."""
+    g = gen(77)
+    side = torch.cuda.Stream()
+    o, z, du = randn(g, 2, 4, 300, 64), randn(g, 2, 300, 256), randn(g, 2, 300, 256)
+    h, y, w = randn(g, 500, 1024), randn(g, 500, 1024), 1 + randn(g, 1024, scale=.2)
+    q, lam = randn(g, 1, 2, 2048, 64), torch.full((2,), 0.9, device=DEV)
+
+    def calls(stream=None):
+        r = list(la2.gated_norm_backward(du, o, z, w[:256], stream=stream))
+        r += la2.residual_norm_backward(h, y, y, w, dh_new=y, post_norm=True, post_weight=w, stream=stream)
+        return r + list(la2.backward(q, q, q, lam, la2.forward(q, q, q, lam, stream=stream), stream=stream))
+    want = calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        got = calls(side)
+        main.wait_stream(side)
+        kept = [t.clone() for t in got]
+        more = [torch.full_like(t, 7) for t in got]
+    for _ in range(3):
+        for t in (*got, *kept, *more):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(torch.equal(a, b) for a, b in zip(kept, want))
+        assert all(bool((t == 7).all()) for t in more)
+    assert la2.last_device_error() == 0
